@@ -69,6 +69,15 @@ typedef enum {
   SVDQ_FORMAT_INT4 = 1   /* signed INT4 codes (qmax 7, §3), bf16 scale per 64 (App. D "16-bit scales") */
 } svdq_format;
 
+/* Element types of the layer norm and of the 8-bit checkpoints. */
+typedef enum { SVDQ_DTYPE_BF16 = 0, SVDQ_DTYPE_FP16 = 1, SVDQ_DTYPE_FP32 = 2 } svdq_dtype;
+
+/* Codes of an 8-bit activation checkpoint (svdq_ckpt8_encode). */
+typedef enum {
+  SVDQ_CKPT8_INT8 = 0, /* integers -127..127 */
+  SVDQ_CKPT8_E4M3 = 1  /* E4M3 values up to 448 */
+} svdq_ckpt8_format;
+
 /* Options of the offline weight transform. */
 typedef struct {
   float alpha;        /* smoothing migration strength (App. D); default 0.5 */
@@ -166,6 +175,25 @@ svdq_status svdq_weights_from_factors_fmt(int N, int K, int rank, const float* i
                                           const uint16_t* L1p_bf16, const uint16_t* L2_bf16,
                                           const float* R, const float* bias, int format, void* stream,
                                           svdq_weights** out);
+
+/*
+ * Builds a handle from stored 4-bit weights, as svdq_weights_export gives them
+ * (a server that loads a quantized checkpoint has no residual to quantize).
+ *   alpha_w   the per-tensor factor: a power of two (1 for INT4)
+ *   codes     host, N x K/2 bytes
+ *   sf        host, the scales in the format's layout: NVFP4
+ *             svdq_act_sf_bytes(N, K) bytes in atoms, INT4 bf16 group-major
+ *             [K/64][round_up(N, 256)]; the values of padding rows are ignored
+ *   inv_lam, L1p_bf16, L2_bf16, bias  as for svdq_weights_from_factors (L2 as
+ *             exported, not divided by alpha_w)
+ *   format    svdq_format
+ * SVDQ_ERR_INVALID_ARG for values that the format does not have: an E4M3 scale
+ * byte above 0x7E, an INT4 scale that is negative or not finite, an INT4 code
+ * of -8.  Synchronizes `stream`.
+ */
+svdq_status svdq_weights_from_codes(int N, int K, int rank, float alpha_w, const uint8_t* codes, const uint8_t* sf,
+                                    const float* inv_lam, const uint16_t* L1p_bf16, const uint16_t* L2_bf16,
+                                    const float* bias, int format, void* stream, svdq_weights** out);
 
 /* The handle's svdq_format. */
 svdq_status svdq_weights_format(const svdq_weights* w, int* format);
@@ -325,7 +353,117 @@ svdq_status svdq_forward_host(const svdq_weights* w, const void* X_host, int M, 
 svdq_status svdq_forward_noalloc(const svdq_weights* w, const void* X_bf16, int M, void* Y_bf16,
                                  void* stream);
 
+/*
+ * The layer for a few tokens with 16-bit activations (W4A16; one token of a
+ * decoder, the modulation layers of a DiT block whose input is one embedding
+ * per image):
+ * Y = bf16_rne(alpha_w * (sum_k fp32(x * inv_lam) deq(wq) + T (L2 / alpha_w)) + b),
+ * T = X L1', sums in fp32.  The activations are not quantized (they enter as
+ * 22-bit values), the weights are those of svdq_linear_w4a4; each is read once
+ * for all tokens.  1 <= M <= 16: for more tokens use svdq_forward.  A token's
+ * result does not depend on the other tokens of the call.
+ *   X_bf16  device, M x K bf16          Y_bf16  device, M x N bf16
+ *   workspace  device memory of at least svdq_linear_w4a16_workspace_bytes(w, M)
+ *              bytes; calls that may run at the same time need one each
+ */
+svdq_status svdq_linear_w4a16(const svdq_weights* w, const void* X_bf16, int M, void* Y_bf16, void* workspace,
+                              size_t workspace_bytes, void* stream);
+size_t svdq_linear_w4a16_workspace_bytes(const svdq_weights* w, int M); /* 0 outside 1 <= M <= 16 */
+
+/*
+ * Layer norm over the K values of each row, with a multiplier and an offset per
+ * channel that a group of consecutive rows shares (all rows: the usual layer
+ * norm; the tokens of one image: adaLN):
+ *   y = (z - mu) * rstd * m + shift,  m = scale, or 1 + scale with plus_one.
+ * Row m belongs to group m / group_rows; the last group may be shorter.
+ * Strides are in elements; 0 means K (rows packed).  Addresses need the
+ * alignment of their elements only; K and strides that are multiples of 8 with
+ * 16-byte aligned addresses are read in whole 16-byte pieces and run faster.
+ */
+typedef struct {
+  int M, K;           /* rows and channels; K <= 16384, M <= 2^30 */
+  int group_rows;     /* rows that share a (scale, shift) vector; 0: all M */
+  int dtype;          /* svdq_dtype of Z, Y, dY and dZ */
+  int param_dtype;    /* svdq_dtype of scale and shift */
+  int plus_one;       /* nonzero: the multiplier is 1 + scale */
+  float eps;          /* added to the variance (forward); finite, >= 0 */
+  int64_t ld_z, ld_y, ld_dy, ld_dz; /* elements between the rows of Z, Y, dY and dZ */
+  int64_t ld_param;   /* elements between the vectors of consecutive groups */
+} svdq_norm_desc;
+
+/*
+ * Forward.  The variance is the mean squared distance from the row's mean,
+ * taken in a second pass over the row in registers; sums are fp32.
+ *   Z       device, M rows of K         Y  device, M rows of K (may be Z itself)
+ *   scale, shift  device, one vector of K per group; NULL: multiplier 1, offset 0
+ *   stats   device, M x 2 floats (mu, rstd) for the backward pass, or NULL
+ *   codes, scales  device, an 8-bit checkpoint of Z in ckpt_format, written from
+ *           the same read (svdq_ckpt8_encode has the layout); both NULL: none
+ */
+svdq_status svdq_layer_norm(const svdq_norm_desc* desc, const void* Z, const void* scale, const void* shift, void* Y,
+                            float* stats, void* codes, void* scales, int ckpt_format, void* stream);
+
+/*
+ * Gradient: with xh = (z - mu) * rstd and g = dY * m,
+ *   dZ = rstd * (g - mean(g) - xh * mean(g * xh))
+ *   dscale = sum over the group's rows of dY * xh,  dshift = sum of dY.
+ *   Z       device, the forward's input; or NULL and its checkpoint in codes and
+ *           scales (ckpt_format): exactly one of the two
+ *   stats   device, M x 2 floats as svdq_layer_norm wrote them
+ *   dZ      device, M rows of K (may be dY itself)
+ *   dscale, dshift  device, one fp32 vector of K per group, packed; each may be NULL
+ *   workspace  device memory of at least svdq_layer_norm_backward_workspace_bytes
+ *           bytes (NULL if that is 0); calls that may run at the same time need
+ *           one each
+ * The column sums are joined in a fixed order: equal calls give equal bits.
+ */
+svdq_status svdq_layer_norm_backward(const svdq_norm_desc* desc, const void* dY, const void* Z, const void* codes,
+                                     const void* scales, int ckpt_format, const float* stats, const void* scale,
+                                     void* dZ, float* dscale, float* dshift, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+size_t svdq_layer_norm_backward_workspace_bytes(int M, int K, int group_rows);
+
+/*
+ * 8-bit activation checkpoint of M rows of K values: `codes` M x K bytes and
+ * `scales` M x ceil(K/32) bytes, one per 32 consecutive values of a row (the
+ * last group may be shorter).  A scale byte b stands for 2^(b - 127), the
+ * smallest such power (b >= 0) at which the group's largest magnitude rounds
+ * to at most 127 (INT8: below 127.5) or is at most 448 (E4M3), but no more than
+ * 2^121 (INT8) or 2^119 (E4M3); a code is the value over the scale, rounded to
+ * nearest, ties to even, and saturated there (so that magnitudes next to 2^128
+ * stay finite).  A group with an
+ * infinity or a NaN gets b = 0xFF and codes 0 and reads back as NaN; other
+ * groups are not affected.
+ *   X       device, M rows of K in dtype (svdq_dtype), ld elements apart (0: K),
+ *           aligned to its elements (16 bytes, K and ld multiples of 8: faster)
+ */
+svdq_status svdq_ckpt8_encode(const void* X, int dtype, int M, int K, int64_t ld, int format, void* codes,
+                              void* scales, void* stream);
+
+/* The values of a checkpoint, code * scale, rounded once to dtype. */
+svdq_status svdq_ckpt8_decode(const void* codes, const void* scales, int M, int K, int format, void* X, int dtype,
+                              int64_t ld, void* stream);
+
+/*
+ * Gradient of a low-rank factor (LoRA or the SVD branch): G = X^T S, summed in
+ * fp32 over the M tokens in a fixed order.  With y = ... + (x A) B the gradient
+ * of A (K x r) is svdq_lowrank_wgrad(X, dY B^T) and that of B^T (N x r) is
+ * svdq_lowrank_wgrad(dY, X A).
+ *   X       device, M x K bf16; or NULL and a checkpoint in codes and scales
+ *           (ckpt_format; its values below 2^-126 may count as 0): exactly one
+ *   S_bf16  device, M x r bf16            G  device, K x r floats
+ *   workspace  device memory of at least svdq_lowrank_wgrad_workspace_bytes bytes
+ *           (NULL if that is 0); calls that may run at the same time need one each
+ * M >= 1, K a positive multiple of 16, 1 <= r <= 128.
+ */
+svdq_status svdq_lowrank_wgrad(const void* X_bf16, const void* codes, const void* scales, int ckpt_format,
+                               const void* S_bf16, int M, int K, int r, float* G, void* workspace,
+                               size_t workspace_bytes, void* stream);
+size_t svdq_lowrank_wgrad_workspace_bytes(int M, int K, int r);
+
 /* Sizes in bytes. */
+size_t svdq_ckpt8_codes_bytes(int M, int K);               /* M * K */
+size_t svdq_ckpt8_scales_bytes(int M, int K);              /* M * ceil(K / 32) */
 size_t svdq_act_codes_bytes(int M, int K);                 /* M * K / 2 */
 size_t svdq_act_sf_bytes(int M, int K);                    /* ceil(M/128)*128 * K/16 */
 size_t svdq_lowrank_bytes(const svdq_weights* w, int M);   /* M * 2 * r_pad * 2 */

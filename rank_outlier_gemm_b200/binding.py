@@ -36,15 +36,26 @@ class PrepareOpts(ctypes.Structure):
                 ("refine_iters", ctypes.c_int), ("format", ctypes.c_int)]
 
 
+class NormDesc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int), ("K", ctypes.c_int), ("group_rows", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("param_dtype", ctypes.c_int), ("plus_one", ctypes.c_int), ("eps", ctypes.c_float),
+                ("ld_z", ctypes.c_int64), ("ld_y", ctypes.c_int64), ("ld_dy", ctypes.c_int64),
+                ("ld_dz", ctypes.c_int64), ("ld_param", ctypes.c_int64)]
+
+
 FORMATS = {"nvfp4": 0, "int4": 1}
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+CKPT8_FORMATS = {"int8": 0, "e4m3": 1}
 
 
 _vp, _i, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+_i64, _desc = ctypes.c_int64, ctypes.POINTER(NormDesc)
 _SIGS = {
     "svdq_prepare_opts_default": (None, [ctypes.POINTER(PrepareOpts)]),
     "svdq_prepare_weights": (_i, [_vp, _vp, _vp, _i, _i, ctypes.POINTER(PrepareOpts), _vp, ctypes.POINTER(_vp)]),
     "svdq_weights_from_factors": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(_vp)]),
     "svdq_weights_from_factors_fmt": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, ctypes.POINTER(_vp)]),
+    "svdq_weights_from_codes": (_i, [_i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, ctypes.POINTER(_vp)]),
     "svdq_weights_format": (_i, [_vp, ctypes.POINTER(_i)]),
     "svdq_weights_sf_bytes": (_sz, [_vp]),
     "svdq_attach_lora": (_i, [_vp, _vp, _vp, _i, _f, _vp]),
@@ -57,6 +68,17 @@ _SIGS = {
     "svdq_norm_quantize_act_lowrank_down": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "svdq_forward_norm": (_i, [_vp, _vp, _i, _vp, _vp, _f, _vp, _vp, _sz, _vp]),
     "svdq_forward_norm_workspace_bytes": (_sz, [_vp, _i]),
+    "svdq_linear_w4a16": (_i, [_vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "svdq_linear_w4a16_workspace_bytes": (_sz, [_vp, _i]),
+    "svdq_layer_norm": (_i, [_desc, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp]),
+    "svdq_layer_norm_backward": (_i, [_desc, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "svdq_layer_norm_backward_workspace_bytes": (_sz, [_i, _i, _i]),
+    "svdq_ckpt8_encode": (_i, [_vp, _i, _i, _i, _i64, _i, _vp, _vp, _vp]),
+    "svdq_ckpt8_decode": (_i, [_vp, _vp, _i, _i, _i, _vp, _i, _i64, _vp]),
+    "svdq_lowrank_wgrad": (_i, [_vp, _vp, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _sz, _vp]),
+    "svdq_lowrank_wgrad_workspace_bytes": (_sz, [_i, _i, _i]),
+    "svdq_ckpt8_codes_bytes": (_sz, [_i, _i]),
+    "svdq_ckpt8_scales_bytes": (_sz, [_i, _i]),
     "svdq_act_codes_bytes": (_sz, [_i, _i]),
     "svdq_act_sf_bytes": (_sz, [_i, _i]),
     "svdq_lowrank_bytes": (_sz, [_vp, _i]),
@@ -136,11 +158,70 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _arg(t, name: str, shape, *dtypes) -> int:
+    """Address of a packed CUDA tensor of this shape and type on the current device."""
+    return _rows_arg(t, name, shape, dtypes, packed=True)[0]
+
+
+def _rows_arg(t, name: str, shape, dtypes, packed: bool = False) -> tuple:
+    """(address, elements between rows) of a CUDA tensor on the current device whose last index is
+    contiguous; `packed`: all of it is."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has type {t.dtype}, not one of {', '.join(str(d) for d in dtypes)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device {torch.cuda.current_device()}")
+    if packed:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr(), 0
+    rows, cols = shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"the last index of {name} must be contiguous")
+    ld = t.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"the rows of {name} overlap")
+    return t.data_ptr(), ld
+
+
+def _workspace(t: Optional[torch.Tensor]) -> tuple:
+    """(address, bytes) of a packed CUDA workspace, or of none."""
+    if t is None:
+        return None, 0
+    n = t.numel() * t.element_size()
+    return (_arg(t, "workspace", t.shape, t.dtype), n) if n else (None, 0)
+
+
+def _shape2(t, name: str) -> tuple:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    return tuple(t.shape)
+
+
+def _ckpt(ckpt, M: int, K: int) -> tuple:
+    """(codes, scales, format) arguments of a checkpoint (codes, scales, "int8" or "e4m3") or of none."""
+    if ckpt is None:
+        return None, None, 0
+    codes, scales, fmt = ckpt
+    return (_arg(codes, "codes", (M, K), torch.uint8), _arg(scales, "scales", (M, (K + 31) // 32), torch.uint8),
+            _ckpt_format(fmt))
+
+
+def _ckpt_format(fmt: str) -> int:
+    if fmt not in CKPT8_FORMATS:
+        raise ValueError(f"checkpoint format {fmt!r} is not one of {', '.join(CKPT8_FORMATS)}")
+    return CKPT8_FORMATS[fmt]
+
+
 class Weights:
     """Owns an svdq_weights handle; destroyed with the object."""
 
     def __init__(self, handle: int):
         self.handle = handle
+        self.N, self.K = self.info["N"], self.info["K"]  # fixed for the handle's life
 
     @property
     def info(self) -> dict:
@@ -194,6 +275,26 @@ def svdq_weights_from_factors(N: int, K: int, rank: int, inv_lam, L1p_bf16, L2_b
     h = _vp()
     _check(_lib.svdq_weights_from_factors_fmt(N, K, rank, ip, lp, l2p, rp, bp, FORMATS[fmt], _stream(stream),
                                               ctypes.byref(h)), "svdq_weights_from_factors_fmt")
+    return Weights(h.value)
+
+
+def svdq_weights_from_codes(N: int, K: int, rank: int, alpha_w: float, codes, sf, inv_lam, L1p_bf16, L2_bf16,
+                            bias=None, fmt: str = "nvfp4", stream=None) -> Weights:
+    """A handle from what svdq_weights_export gives (host arrays)."""
+    cp, ck = _host(codes, np.uint8)
+    sp, sk = _host(sf, np.uint8)
+    ip, ik = _host(inv_lam, np.float32)
+    lp, lk = _host(L1p_bf16, np.uint16) if rank else (None, None)
+    l2p, l2k = _host(L2_bf16, np.uint16) if rank else (None, None)
+    bp, bk = _host(bias, np.float32)
+    n_sf = (K // 64) * (-(-N // 256) * 256) * 2 if fmt == "int4" else svdq_act_sf_bytes(N, K)
+    for a, n, name in ((ck, N * K // 2, "codes"), (sk, n_sf, "sf"), (ik, K, "inv_lam"), (lk, K * rank, "L1p"),
+                       (l2k, rank * N, "L2"), (bk, N, "bias")):
+        if a is not None and a.size != n:
+            raise ValueError(f"{name} has {a.size} elements, not {n}")
+    h = _vp()
+    _check(_lib.svdq_weights_from_codes(N, K, rank, alpha_w, cp, sp, ip, lp, l2p, bp, FORMATS[fmt], _stream(stream),
+                                        ctypes.byref(h)), "svdq_weights_from_codes")
     return Weights(h.value)
 
 
@@ -276,6 +377,123 @@ def svdq_forward_norm(w: Weights, Z: torch.Tensor, norm_a: torch.Tensor, norm_c:
 
 def svdq_forward_norm_workspace_bytes(w: Weights, M: int) -> int:
     return _lib.svdq_forward_norm_workspace_bytes(w.handle, M)
+
+
+def svdq_linear_w4a16(w: Weights, X: torch.Tensor, Y: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """The layer on 1..16 tokens with 16-bit activations: X [M, K], Y [M, N], CUDA bf16."""
+    M, K = _shape2(X, "X")
+    ws, n = _workspace(workspace)
+    if K != w.K:
+        raise ValueError(f"X has {K} columns, the layer takes {w.K}")
+    _check(_lib.svdq_linear_w4a16(w.handle, _arg(X, "X", (M, K), torch.bfloat16), M,
+                                  _arg(Y, "Y", (M, w.N), torch.bfloat16), ws, n, _stream(stream)), "svdq_linear_w4a16")
+
+
+def svdq_linear_w4a16_workspace_bytes(w: Weights, M: int) -> int:
+    return _lib.svdq_linear_w4a16_workspace_bytes(w.handle, M)
+
+
+def _norm_params(scale, shift, M: int, K: int, group_rows: int) -> tuple:
+    """(svdq_dtype, elements between groups, addresses) of the per-group vectors [groups, K]."""
+    groups = -(-M // (group_rows or M)) if M else 0
+    dtype, ld, ptrs = torch.float32, 0, []
+    for p, name in ((scale, "scale"), (shift, "shift")):
+        if p is None:
+            ptrs.append(None)
+            continue
+        if ptrs and ptrs[0] is not None and p.dtype != scale.dtype:
+            raise ValueError("scale and shift must have the same type")
+        at, stride = _rows_arg(p, name, (groups, K), DTYPES)
+        if ptrs and ptrs[0] is not None and stride != ld:
+            raise ValueError("scale and shift must have the same stride")
+        dtype, ld = p.dtype, stride
+        ptrs.append(at)
+    return DTYPES[dtype], ld, ptrs[0], ptrs[1]
+
+
+def svdq_layer_norm(Z: torch.Tensor, scale: Optional[torch.Tensor], shift: Optional[torch.Tensor], Y: torch.Tensor,
+                    stats: Optional[torch.Tensor], eps: float, group_rows: int = 0, plus_one: bool = False, ckpt=None,
+                    stream=None) -> None:
+    """Layer norm of the rows of a CUDA [M, K] tensor (bf16, fp16 or fp32) into Y.
+
+    scale and shift are [groups, K] (one row per group_rows rows of Z, 0: all), stats float32 [M, 2];
+    ckpt = (codes, scales, "int8" or "e4m3") also writes Z's 8-bit checkpoint (uint8 [M, K] and
+    [M, ceil(K/32)]).
+    """
+    M, K = _shape2(Z, "Z")
+    zp, ld_z = _rows_arg(Z, "Z", (M, K), DTYPES)
+    yp, ld_y = _rows_arg(Y, "Y", (M, K), (Z.dtype,))
+    pd, ld_p, sp, hp = _norm_params(scale, shift, M, K, group_rows)
+    d = NormDesc(M, K, group_rows, DTYPES[Z.dtype], pd, plus_one, eps, ld_z, ld_y, 0, 0, ld_p)
+    codes, scales, fmt = _ckpt(ckpt, M, K)
+    _check(_lib.svdq_layer_norm(d, zp, sp, hp, yp, _arg(stats, "stats", (M, 2), torch.float32) if stats is not None else None,
+                                codes, scales, fmt, _stream(stream)), "svdq_layer_norm")
+
+
+def svdq_layer_norm_backward(dY: torch.Tensor, Z: Optional[torch.Tensor], stats: torch.Tensor,
+                             scale: Optional[torch.Tensor], dZ: torch.Tensor, dscale: Optional[torch.Tensor],
+                             dshift: Optional[torch.Tensor], workspace: Optional[torch.Tensor], group_rows: int = 0,
+                             plus_one: bool = False, ckpt=None, stream=None) -> None:
+    """Gradient of svdq_layer_norm from Z or (Z None) from its checkpoint; dscale and dshift float32 [groups, K]."""
+    M, K = _shape2(dY, "dY")
+    dyp, ld_dy = _rows_arg(dY, "dY", (M, K), DTYPES)
+    dzp, ld_dz = _rows_arg(dZ, "dZ", (M, K), (dY.dtype,))
+    zp, ld_z = _rows_arg(Z, "Z", (M, K), (dY.dtype,)) if Z is not None else (None, 0)
+    pd, ld_p, sp, _ = _norm_params(scale, None, M, K, group_rows)
+    groups = -(-M // (group_rows or M)) if M else 0
+    grads = [_arg(g, name, (groups, K), torch.float32) if g is not None else None
+             for g, name in ((dscale, "dscale"), (dshift, "dshift"))]
+    d = NormDesc(M, K, group_rows, DTYPES[dY.dtype], pd, plus_one, 0.0, ld_z, 0, ld_dy, ld_dz, ld_p)
+    codes, scales, fmt = _ckpt(ckpt, M, K)
+    ws, n = _workspace(workspace)
+    _check(_lib.svdq_layer_norm_backward(d, dyp, zp, codes, scales, fmt, _arg(stats, "stats", (M, 2), torch.float32), sp,
+                                         dzp, grads[0], grads[1], ws, n, _stream(stream)), "svdq_layer_norm_backward")
+
+
+def svdq_layer_norm_backward_workspace_bytes(M: int, K: int, group_rows: int = 0) -> int:
+    return _lib.svdq_layer_norm_backward_workspace_bytes(M, K, group_rows)
+
+
+def svdq_ckpt8_encode(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, fmt: str = "int8",
+                      stream=None) -> None:
+    """8-bit checkpoint of a CUDA [M, K] tensor (bf16, fp16 or fp32) into uint8 [M, K] and [M, ceil(K/32)]."""
+    M, K = _shape2(X, "X")
+    xp, ld = _rows_arg(X, "X", (M, K), DTYPES)
+    cp, sp, f = _ckpt((codes, scales, fmt), M, K)
+    _check(_lib.svdq_ckpt8_encode(xp, DTYPES[X.dtype], M, K, ld, f, cp, sp, _stream(stream)), "svdq_ckpt8_encode")
+
+
+def svdq_ckpt8_decode(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, fmt: str = "int8",
+                      stream=None) -> None:
+    """The values of a checkpoint into a CUDA [M, K] tensor (bf16, fp16 or fp32)."""
+    M, K = _shape2(X, "X")
+    xp, ld = _rows_arg(X, "X", (M, K), DTYPES)
+    cp, sp, f = _ckpt((codes, scales, fmt), M, K)
+    _check(_lib.svdq_ckpt8_decode(cp, sp, M, K, f, xp, DTYPES[X.dtype], ld, _stream(stream)), "svdq_ckpt8_decode")
+
+
+def svdq_lowrank_wgrad(X: Optional[torch.Tensor], S: torch.Tensor, G: torch.Tensor, workspace: Optional[torch.Tensor],
+                       ckpt=None, stream=None) -> None:
+    """G [K, r] float32 = X^T S for CUDA bf16 X [M, K] (or, X None, its checkpoint) and S [M, r]."""
+    M, r = _shape2(S, "S")
+    K = _shape2(G, "G")[0]
+    xp = _arg(X, "X", (M, K), torch.bfloat16) if X is not None else None
+    codes, scales, fmt = _ckpt(ckpt, M, K)
+    ws, n = _workspace(workspace)
+    _check(_lib.svdq_lowrank_wgrad(xp, codes, scales, fmt, _arg(S, "S", (M, r), torch.bfloat16), M, K, r,
+                                   _arg(G, "G", (K, r), torch.float32), ws, n, _stream(stream)), "svdq_lowrank_wgrad")
+
+
+def svdq_lowrank_wgrad_workspace_bytes(M: int, K: int, r: int) -> int:
+    return _lib.svdq_lowrank_wgrad_workspace_bytes(M, K, r)
+
+
+def svdq_ckpt8_codes_bytes(M: int, K: int) -> int:
+    return _lib.svdq_ckpt8_codes_bytes(M, K)
+
+
+def svdq_ckpt8_scales_bytes(M: int, K: int) -> int:
+    return _lib.svdq_ckpt8_scales_bytes(M, K)
 
 
 def svdq_act_codes_bytes(M: int, K: int) -> int:

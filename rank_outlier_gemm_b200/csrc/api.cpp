@@ -164,6 +164,32 @@ svdq_status upload_lowrank(svdq_weights* w, cudaStream_t stream) {
                       static_cast<uint64_t>(rp) * 2, 32, 128, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+// Byte of row n, 16-wide group c in the block-scale layout (128-row x 4-column atoms of 512 bytes).
+size_t sf_atom_index(int n, int c, int K) {
+  return (static_cast<size_t>(n / 128) * (K / 64) + c / 4) * 512 + (n % 32) * 16 + (n % 128) / 32 * 4 + c % 4;
+}
+
+// Rows of the weight scales: padded to 128 (NVFP4 atoms) or 256 (INT4).
+int scale_rows(int N, int format) { return format == SVDQ_FORMAT_INT4 ? round_up(N, 256) : round_up(N, 128); }
+
+// Tensor maps over a handle's codes and scales.
+svdq_status make_weight_maps(svdq_weights* w) {
+  const int K = w->K, N = w->N;
+  if (w->format == SVDQ_FORMAT_INT4)  // one 64-wide group (32 bytes) of 256 rows per load
+    return make_tmap_2d(&w->map_wq_256, w->d_wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, N, K / 2, 32, 256,
+                        CU_TENSOR_MAP_SWIZZLE_NONE);
+  SVDQ_TRY(make_tmap_2d(&w->map_wq_256, w->d_wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, N, K / 2, 128, 256,
+                        CU_TENSOR_MAP_SWIZZLE_128B));
+  SVDQ_TRY(make_tmap_2d(&w->map_wq_128, w->d_wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, N, K / 2, 128, 128,
+                        CU_TENSOR_MAP_SWIZZLE_128B));
+  // scale atoms [npad/128][K/64][512 bytes] as 32-bit words
+  const uint64_t dims[3] = {128, static_cast<uint64_t>(K / 64),
+                            static_cast<uint64_t>(scale_rows(N, w->format) / 128)};
+  const uint64_t strides[2] = {512, static_cast<uint64_t>(K / 64) * 512};
+  const uint32_t box[3] = {128, 4, 2};
+  return make_tmap_3d(&w->map_wsf, w->d_wsf, CU_TENSOR_MAP_DATA_TYPE_UINT32, dims, strides, box);
+}
+
 svdq_status build_handle(int N, int K, int rank, const float* inv_lam, const uint16_t* L1p,
                          const uint16_t* L2, const float* R, const float* bias, int keep_residual, int format,
                          cudaStream_t stream, svdq_weights** out) {
@@ -193,7 +219,7 @@ svdq_status build_handle(int N, int K, int rank, const float* inv_lam, const uin
   for (size_t i = 0; i < nk; ++i) Rp[i] = static_cast<float>(static_cast<double>(R[i]) / w->alpha_w);
   if (keep_residual) w->residual = Rp;
 
-  const int npad = format == SVDQ_FORMAT_INT4 ? round_up(N, 256) : round_up(N, 128);
+  const int npad = scale_rows(N, format);
   const size_t sf_bytes = format == SVDQ_FORMAT_INT4 ? static_cast<size_t>(K / 64) * npad * 2
                                                       : static_cast<size_t>(npad) * (K / 16);
   cudaError_t e;
@@ -242,24 +268,64 @@ svdq_status build_handle(int N, int K, int rank, const float* inv_lam, const uin
   if (st != SVDQ_OK) return bail(st);
   st = upload_lowrank(w, stream);
   if (st != SVDQ_OK) return bail(st);
-  if (format == SVDQ_FORMAT_INT4) {  // one 64-wide group (32 bytes) of 256 rows per load
-    st = make_tmap_2d(&w->map_wq_256, w->d_wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, N, K / 2, 32, 256,
-                      CU_TENSOR_MAP_SWIZZLE_NONE);
-    if (st != SVDQ_OK) return bail(st);
-    *out = w;
-    return SVDQ_OK;
+  if ((st = make_weight_maps(w)) != SVDQ_OK) return bail(st);
+  *out = w;
+  return SVDQ_OK;
+}
+
+// A handle from stored codes and scales (host), the padding rows' scales cleared.
+svdq_status build_from_codes(int N, int K, int rank, float alpha_w, const uint8_t* codes, const uint8_t* sf,
+                             const float* inv_lam, const uint16_t* L1p, const uint16_t* L2, const float* bias,
+                             int format, cudaStream_t stream, svdq_weights** out) {
+  svdq_weights* w = new (std::nothrow) svdq_weights();
+  if (!w) return fail(SVDQ_ERR_OOM, "host allocation failed");
+  auto bail = [&](svdq_status s) {
+    free_device(w);
+    delete w;
+    return s;
+  };
+  cudaGetDevice(&w->device);
+  w->N = N;
+  w->K = K;
+  w->rank = rank;
+  w->format = format;
+  w->alpha_w = alpha_w;
+  w->inv_lam.assign(inv_lam, inv_lam + K);
+  if (rank > 0) {
+    w->L1p.assign(L1p, L1p + static_cast<size_t>(K) * rank);
+    w->L2.assign(L2, L2 + static_cast<size_t>(rank) * N);
   }
-  st = make_tmap_2d(&w->map_wq_256, w->d_wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, N, K / 2, 128, 256,
-                    CU_TENSOR_MAP_SWIZZLE_128B);
-  if (st == SVDQ_OK)
-    st = make_tmap_2d(&w->map_wq_128, w->d_wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, N, K / 2, 128, 128,
-                      CU_TENSOR_MAP_SWIZZLE_128B);
-  if (st == SVDQ_OK) {  // scale atoms [npad/128][K/64][512 bytes] as 32-bit words
-    const uint64_t dims[3] = {128, static_cast<uint64_t>(K / 64), static_cast<uint64_t>(npad / 128)};
-    const uint64_t strides[2] = {512, static_cast<uint64_t>(K / 64) * 512};
-    const uint32_t box[3] = {128, 4, 2};
-    st = make_tmap_3d(&w->map_wsf, w->d_wsf, CU_TENSOR_MAP_DATA_TYPE_UINT32, dims, strides, box);
+  w->bias.assign(N, 0.0f);
+  if (bias) std::copy(bias, bias + N, w->bias.begin());
+  std::vector<float> bias_pad(static_cast<size_t>(round_up(N, 256)), 0.0f);
+  std::copy(w->bias.begin(), w->bias.end(), bias_pad.begin());
+  const size_t nk = static_cast<size_t>(N) * K;
+  const int npad = scale_rows(N, format);
+  std::vector<uint8_t> scales;
+  if (format == SVDQ_FORMAT_INT4) {
+    scales.assign(sf, sf + static_cast<size_t>(K / 64) * npad * 2);
+    for (int g = 0; g < K / 64; ++g)
+      std::fill(scales.begin() + (static_cast<size_t>(g) * npad + N) * 2,
+                scales.begin() + static_cast<size_t>(g + 1) * npad * 2, uint8_t{0});
+  } else {
+    scales.assign(sf, sf + static_cast<size_t>(npad) * (K / 16));
+    for (int n = N; n < npad; ++n)
+      for (int c = 0; c < K / 16; ++c) scales[sf_atom_index(n, c, K)] = 0;
   }
+  cudaError_t e = cudaSuccess;
+  auto upload = [&](auto** dst, const void* src, size_t bytes) {
+    if (e == cudaSuccess) e = cudaMalloc(dst, bytes);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(*dst, src, bytes, cudaMemcpyHostToDevice, stream);
+  };
+  upload(&w->d_wq, codes, nk / 2);
+  upload(&w->d_wsf, scales.data(), scales.size());
+  upload(&w->d_inv_lam, inv_lam, static_cast<size_t>(K) * 4);
+  upload(&w->d_bias, bias_pad.data(), bias_pad.size() * 4);
+  const cudaError_t synced = cudaStreamSynchronize(stream);  // the host copies end with this call
+  if (e == cudaSuccess) e = synced;
+  if (e != cudaSuccess) return bail(cuda_fail(e, "upload of the weights"));
+  svdq_status st = upload_lowrank(w, stream);
+  if (st == SVDQ_OK) st = make_weight_maps(w);
   if (st != SVDQ_OK) return bail(st);
   *out = w;
   return SVDQ_OK;
@@ -285,6 +351,14 @@ svdq_status check_runtime(const svdq_weights* w, int M) {
 svdq_status check_dev_ptr(const void* p, const char* name) {
   if (!p) return fail(SVDQ_ERR_INVALID_ARG, "%s is null", name);
   if (!aligned16(p)) return fail(SVDQ_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+  return SVDQ_OK;
+}
+
+// Caller's scratch memory; a call that needs none takes a null one.
+svdq_status check_workspace(const void* p, size_t bytes, size_t need) {
+  if (need == 0) return SVDQ_OK;
+  SVDQ_TRY(check_dev_ptr(p, "workspace"));
+  if (bytes < need) return fail(SVDQ_ERR_INVALID_ARG, "workspace has %zu bytes, needs %zu", bytes, need);
   return SVDQ_OK;
 }
 
@@ -428,6 +502,52 @@ svdq_status svdq_weights_from_factors_fmt(int N, int K, int rank, const float* i
   SVDQ_TRY(check_device());
   return build_handle(N, K, rank, inv_lam, L1p_bf16, L2_bf16, R, bias, 1, format, static_cast<cudaStream_t>(stream),
                       out);
+}
+
+svdq_status svdq_weights_from_codes(int N, int K, int rank, float alpha_w, const uint8_t* codes, const uint8_t* sf,
+                                    const float* inv_lam, const uint16_t* L1p_bf16, const uint16_t* L2_bf16,
+                                    const float* bias, int format, void* stream, svdq_weights** out) {
+  if (!out) return fail(SVDQ_ERR_INVALID_ARG, "out is null");
+  *out = nullptr;
+  SVDQ_TRY(check_shape(N, K));
+  if (format != SVDQ_FORMAT_NVFP4 && format != SVDQ_FORMAT_INT4)
+    return fail(SVDQ_ERR_INVALID_ARG, "format=%d is neither NVFP4 (0) nor INT4 (1)", format);
+  if (rank < 0 || rank > 128) return fail(SVDQ_ERR_INVALID_ARG, "rank=%d must be in [0, 128]", rank);
+  if (!codes || !sf || !inv_lam) return fail(SVDQ_ERR_INVALID_ARG, "codes, sf and inv_lam are required");
+  if (rank > 0 && (!L1p_bf16 || !L2_bf16)) return fail(SVDQ_ERR_INVALID_ARG, "rank > 0 needs L1p and L2");
+  int exp2 = 0;
+  if (!std::isfinite(alpha_w) || alpha_w <= 0 || std::frexp(alpha_w, &exp2) != 0.5f)
+    return fail(SVDQ_ERR_INVALID_ARG, "alpha_w=%g must be a power of two", alpha_w);
+  if (format == SVDQ_FORMAT_INT4 && alpha_w != 1.0f)
+    return fail(SVDQ_ERR_INVALID_ARG, "alpha_w=%g must be 1 for INT4", alpha_w);
+  for (int k = 0; k < K; ++k)
+    if (!std::isfinite(inv_lam[k])) return fail(SVDQ_ERR_INVALID_ARG, "inv_lam has a non-finite value");
+  if (format == SVDQ_FORMAT_INT4) {
+    const int npad = scale_rows(N, format);
+    for (int g = 0; g < K / 64; ++g)
+      for (int n = 0; n < N; ++n) {
+        uint16_t s;
+        std::memcpy(&s, sf + (static_cast<size_t>(g) * npad + n) * 2, 2);
+        if (s >= 0x7F80) return fail(SVDQ_ERR_INVALID_ARG, "sf has a negative or non-finite scale");
+      }
+    const size_t bytes = static_cast<size_t>(N) * K / 2;  // a multiple of 8
+    for (size_t i = 0; i < bytes; i += 8) {
+      uint64_t v;
+      std::memcpy(&v, codes + i, 8);
+      v ^= 0x8888888888888888ull;  // a code of -8 becomes a zero nibble
+      const uint64_t low = v & 0x7777777777777777ull;
+      if (((low + 0x7777777777777777ull) | v | 0x7777777777777777ull) != ~0ull)
+        return fail(SVDQ_ERR_INVALID_ARG, "codes has an INT4 code of -8");
+    }
+  } else {
+    for (int n = 0; n < N; ++n)
+      for (int c = 0; c < K / 16; ++c)
+        if (sf[sf_atom_index(n, c, K)] > 0x7E)
+          return fail(SVDQ_ERR_INVALID_ARG, "sf has a negative or NaN E4M3 scale");
+  }
+  SVDQ_TRY(check_device());
+  return build_from_codes(N, K, rank, alpha_w, codes, sf, inv_lam, L1p_bf16, L2_bf16, bias, format,
+                          static_cast<cudaStream_t>(stream), out);
 }
 
 svdq_status svdq_weights_format(const svdq_weights* w, int* format) {
@@ -690,6 +810,182 @@ svdq_status svdq_forward_host(const svdq_weights* w, const void* X_host, int M, 
   SVDQ_CUDA_TRY(cudaEventRecord(hp->done, hp->out));
   SVDQ_CUDA_TRY(cudaStreamWaitEvent(s, hp->done, 0));
   return SVDQ_OK;
+}
+
+size_t svdq_linear_w4a16_workspace_bytes(const svdq_weights* w, int M) {
+  return w && M >= 1 && M <= 16 ? w4a16_workspace(M, w->K, w->r_pad) : 0;
+}
+
+svdq_status svdq_linear_w4a16(const svdq_weights* w, const void* X_bf16, int M, void* Y_bf16, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (w && M > 16) return fail(SVDQ_ERR_INVALID_ARG, "M=%d must be <= 16 (svdq_forward takes more tokens)", M);
+  SVDQ_TRY(check_runtime(w, M));
+  SVDQ_TRY(check_dev_ptr(X_bf16, "X"));
+  SVDQ_TRY(check_dev_ptr(Y_bf16, "Y"));
+  SVDQ_TRY(check_workspace(workspace, workspace_bytes, w4a16_workspace(M, w->K, w->r_pad)));
+  return launch_w4a16(w, X_bf16, M, Y_bf16, workspace, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+svdq_status check_dtype(int dtype, const char* name) {
+  if (dtype < SVDQ_DTYPE_BF16 || dtype > SVDQ_DTYPE_FP32)
+    return fail(SVDQ_ERR_INVALID_ARG, "%s=%d is not an svdq_dtype", name, dtype);
+  return SVDQ_OK;
+}
+
+svdq_status check_ckpt_format(int format) {
+  if (format != SVDQ_CKPT8_INT8 && format != SVDQ_CKPT8_E4M3)
+    return fail(SVDQ_ERR_INVALID_ARG, "checkpoint format=%d is neither INT8 (0) nor E4M3 (1)", format);
+  return SVDQ_OK;
+}
+
+// A required device pointer that needs the alignment of its elements only.
+svdq_status check_elem_ptr(const void* p, int dtype, const char* name) {
+  if (!p) return fail(SVDQ_ERR_INVALID_ARG, "%s is null", name);
+  if (reinterpret_cast<uintptr_t>(p) % (dtype == SVDQ_DTYPE_FP32 ? 4 : 2))
+    return fail(SVDQ_ERR_INVALID_ARG, "%s is not aligned to its elements", name);
+  return SVDQ_OK;
+}
+
+svdq_status check_ld(int64_t* ld, int K, const char* name) {
+  if (*ld == 0) *ld = K;
+  // 2^40 elements bound every address below 2^63 for M <= 2^30 rows of a real allocation
+  if (*ld < K || *ld > (1ll << 40)) return fail(SVDQ_ERR_INVALID_ARG, "%s is below K=%d or too large", name, K);
+  return SVDQ_OK;
+}
+
+svdq_status check_rows(int M, int K, int max_k) {
+  if (M < 1 || M > (1 << 30)) return fail(SVDQ_ERR_INVALID_ARG, "M=%d must be in [1, 2^30]", M);
+  if (K < 1 || K > max_k) return fail(SVDQ_ERR_INVALID_ARG, "K=%d must be in [1, %d]", K, max_k);
+  return SVDQ_OK;
+}
+
+svdq_status norm_args(const svdq_norm_desc* d, NormArgs* a) {
+  if (!d) return fail(SVDQ_ERR_INVALID_ARG, "desc is null");
+  SVDQ_TRY(check_rows(d->M, d->K, kNormMaxK));
+  SVDQ_TRY(check_dtype(d->dtype, "dtype"));
+  SVDQ_TRY(check_dtype(d->param_dtype, "param_dtype"));
+  if (d->group_rows < 0) return fail(SVDQ_ERR_INVALID_ARG, "group_rows=%d must be >= 0", d->group_rows);
+  if (!(d->eps >= 0.0f) || !std::isfinite(d->eps)) return fail(SVDQ_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  *a = NormArgs{d->M, d->K, d->group_rows && d->group_rows < d->M ? d->group_rows : d->M, d->dtype, d->param_dtype,
+                d->plus_one, d->eps, d->ld_z, d->ld_y, d->ld_dy, d->ld_dz, d->ld_param};
+  SVDQ_TRY(check_ld(&a->ld_z, a->K, "ld_z"));
+  SVDQ_TRY(check_ld(&a->ld_y, a->K, "ld_y"));
+  SVDQ_TRY(check_ld(&a->ld_dy, a->K, "ld_dy"));
+  SVDQ_TRY(check_ld(&a->ld_dz, a->K, "ld_dz"));
+  return check_ld(&a->ld_param, a->K, "ld_param");
+}
+
+// 0 no checkpoint, 1 a complete one
+svdq_status check_ckpt(const void* codes, const void* scales, int format, int* has) {
+  if (!codes != !scales) return fail(SVDQ_ERR_INVALID_ARG, "a checkpoint needs both codes and scales");
+  *has = codes != nullptr;
+  if (!*has) return SVDQ_OK;
+  SVDQ_TRY(check_ckpt_format(format));
+  return check_dev_ptr(codes, "codes");
+}
+
+}  // namespace
+
+svdq_status svdq_layer_norm(const svdq_norm_desc* desc, const void* Z, const void* scale, const void* shift, void* Y,
+                            float* stats, void* codes, void* scales, int ckpt_format, void* stream) {
+  NormArgs a;
+  int has = 0;
+  SVDQ_TRY(norm_args(desc, &a));
+  SVDQ_TRY(check_elem_ptr(Z, a.dtype, "Z"));
+  SVDQ_TRY(check_elem_ptr(Y, a.dtype, "Y"));
+  if (scale) SVDQ_TRY(check_elem_ptr(scale, a.param_dtype, "scale"));
+  if (shift) SVDQ_TRY(check_elem_ptr(shift, a.param_dtype, "shift"));
+  if (stats) SVDQ_TRY(check_dev_ptr(stats, "stats"));
+  SVDQ_TRY(check_ckpt(codes, scales, ckpt_format, &has));
+  SVDQ_TRY(check_device());
+  return launch_layer_norm(a, Z, scale, shift, Y, stats, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales),
+                           ckpt_format, static_cast<cudaStream_t>(stream));
+}
+
+size_t svdq_layer_norm_backward_workspace_bytes(int M, int K, int group_rows) {
+  if (M < 1 || M > (1 << 30) || K < 1 || K > kNormMaxK || group_rows < 0) return 0;
+  return layer_norm_backward_workspace(M, K, group_rows && group_rows < M ? group_rows : M);
+}
+
+svdq_status svdq_layer_norm_backward(const svdq_norm_desc* desc, const void* dY, const void* Z, const void* codes,
+                                     const void* scales, int ckpt_format, const float* stats, const void* scale,
+                                     void* dZ, float* dscale, float* dshift, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  NormArgs a;
+  int has = 0;
+  SVDQ_TRY(norm_args(desc, &a));
+  SVDQ_TRY(check_ckpt(codes, scales, ckpt_format, &has));
+  if (has == (Z != nullptr)) return fail(SVDQ_ERR_INVALID_ARG, "give either Z or its checkpoint");
+  if (Z) SVDQ_TRY(check_elem_ptr(Z, a.dtype, "Z"));
+  SVDQ_TRY(check_elem_ptr(dY, a.dtype, "dY"));
+  SVDQ_TRY(check_elem_ptr(dZ, a.dtype, "dZ"));
+  if (scale) SVDQ_TRY(check_elem_ptr(scale, a.param_dtype, "scale"));
+  SVDQ_TRY(check_dev_ptr(stats, "stats"));
+  if (dscale) SVDQ_TRY(check_elem_ptr(dscale, SVDQ_DTYPE_FP32, "dscale"));
+  if (dshift) SVDQ_TRY(check_elem_ptr(dshift, SVDQ_DTYPE_FP32, "dshift"));
+  SVDQ_TRY(check_workspace(workspace, workspace_bytes, layer_norm_backward_workspace(a.M, a.K, a.rows)));
+  SVDQ_TRY(check_device());
+  return launch_layer_norm_backward(a, dY, Z, static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales),
+                                    ckpt_format, stats, scale, dZ, dscale, dshift, workspace,
+                                    static_cast<cudaStream_t>(stream));
+}
+
+svdq_status svdq_ckpt8_encode(const void* X, int dtype, int M, int K, int64_t ld, int format, void* codes,
+                              void* scales, void* stream) {
+  SVDQ_TRY(check_rows(M, K, 1 << 30));
+  SVDQ_TRY(check_dtype(dtype, "dtype"));
+  SVDQ_TRY(check_ckpt_format(format));
+  SVDQ_TRY(check_ld(&ld, K, "ld"));
+  SVDQ_TRY(check_elem_ptr(X, dtype, "X"));
+  SVDQ_TRY(check_dev_ptr(codes, "codes"));
+  if (!scales) return fail(SVDQ_ERR_INVALID_ARG, "scales is null");
+  SVDQ_TRY(check_device());
+  return launch_ckpt8_encode(X, dtype, M, K, ld, format, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales),
+                             static_cast<cudaStream_t>(stream));
+}
+
+svdq_status svdq_ckpt8_decode(const void* codes, const void* scales, int M, int K, int format, void* X, int dtype,
+                              int64_t ld, void* stream) {
+  SVDQ_TRY(check_rows(M, K, 1 << 30));
+  SVDQ_TRY(check_dtype(dtype, "dtype"));
+  SVDQ_TRY(check_ckpt_format(format));
+  SVDQ_TRY(check_ld(&ld, K, "ld"));
+  SVDQ_TRY(check_elem_ptr(X, dtype, "X"));
+  SVDQ_TRY(check_dev_ptr(codes, "codes"));
+  if (!scales) return fail(SVDQ_ERR_INVALID_ARG, "scales is null");
+  SVDQ_TRY(check_device());
+  return launch_ckpt8_decode(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), M, K, format, X,
+                             dtype, ld, static_cast<cudaStream_t>(stream));
+}
+
+size_t svdq_lowrank_wgrad_workspace_bytes(int M, int K, int r) {
+  return M >= 1 && M <= (1 << 30) && K >= 16 && K % 16 == 0 && r >= 1 && r <= 128 ? lowrank_wgrad_workspace(M, K, r) : 0;
+}
+
+svdq_status svdq_lowrank_wgrad(const void* X_bf16, const void* codes, const void* scales, int ckpt_format,
+                               const void* S_bf16, int M, int K, int r, float* G, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  int has = 0;
+  SVDQ_TRY(check_rows(M, K, 1 << 30));
+  if (K % 16) return fail(SVDQ_ERR_INVALID_ARG, "K=%d must be a multiple of 16", K);
+  if (r < 1 || r > 128) return fail(SVDQ_ERR_INVALID_ARG, "r=%d must be in [1, 128]", r);
+  SVDQ_TRY(check_ckpt(codes, scales, ckpt_format, &has));
+  if (has == (X_bf16 != nullptr)) return fail(SVDQ_ERR_INVALID_ARG, "give either X or its checkpoint");
+  if (X_bf16) SVDQ_TRY(check_dev_ptr(X_bf16, "X"));
+  SVDQ_TRY(check_dev_ptr(S_bf16, "S"));
+  SVDQ_TRY(check_dev_ptr(G, "G"));
+  SVDQ_TRY(check_workspace(workspace, workspace_bytes, lowrank_wgrad_workspace(M, K, r)));
+  SVDQ_TRY(check_device());
+  const int src = !has ? 0 : ckpt_format == SVDQ_CKPT8_INT8 ? 1 : 2;
+  return launch_lowrank_wgrad(has ? codes : X_bf16, static_cast<const uint8_t*>(scales), src, S_bf16, M, K, r, G,
+                              workspace, static_cast<cudaStream_t>(stream));
+}
+
+size_t svdq_ckpt8_codes_bytes(int M, int K) { return M > 0 && K > 0 ? static_cast<size_t>(M) * K : 0; }
+size_t svdq_ckpt8_scales_bytes(int M, int K) {
+  return M > 0 && K > 0 ? static_cast<size_t>(M) * ((static_cast<size_t>(K) + 31) / 32) : 0;
 }
 
 int svdq_weights_rank(const svdq_weights* w) { return w ? w->rank : -1; }

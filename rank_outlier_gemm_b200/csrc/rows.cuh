@@ -1,0 +1,262 @@
+// Row operands of the layer norm and checkpoint kernels: eight values at a time as fp32, and the
+// 8-bit checkpoint codec.
+//
+// A team of `threads` (a multiple of 32) threads covers a row of K columns in one of two layouts:
+//   vector   thread t owns columns 8 (i threads + t) + j, j < 8: one 16-byte access per 8 values
+//            (two for fp32); K, the row strides and the addresses allow it
+//   element  thread t owns columns (8 i + j) threads + t: any K, stride and alignment, 2- or 4-byte
+//            accesses that are contiguous over a warp
+// A checkpoint group (32 consecutive columns) is 4 neighbouring threads' vectors in the first and
+// one j of a whole warp in the second, so its largest magnitude is a warp shuffle away.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "svdq.h"
+
+namespace svdq {
+namespace dev {
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// One bf16 pair as fp32 (a bf16 is the top half of an fp32).
+__device__ __forceinline__ float pair_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float pair_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Eight consecutive values (16-byte aligned for 16-bit types, two aligned halves for fp32).
+__device__ __forceinline__ void unpack8(const uint4& a, float (&v)[8], const __nv_bfloat16*) {
+  v[0] = pair_lo(a.x), v[1] = pair_hi(a.x), v[2] = pair_lo(a.y), v[3] = pair_hi(a.y);
+  v[4] = pair_lo(a.z), v[5] = pair_hi(a.z), v[6] = pair_lo(a.w), v[7] = pair_hi(a.w);
+}
+__device__ __forceinline__ void unpack8(const uint4& a, float (&v)[8], const __half*) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+    v[2 * j] = f.x, v[2 * j + 1] = f.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  unpack8(*reinterpret_cast<const uint4*>(p), v, p);
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint4 a;
+  uint32_t* w = &a.x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = a;
+}
+__device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
+  uint4 a;
+  uint32_t* w = &a.x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = a;
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// Column of value j of chunk i of thread t.
+template <bool VEC>
+__device__ __forceinline__ int row_column(int i, int j, int t, int threads) {
+  return VEC ? (i * threads + t) * 8 + j : (i * 8 + j) * threads + t;
+}
+
+// Chunk i of a row: columns beyond K give `fill`.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_chunk(const T* row, int K, int i, int t, int threads, float fill, float (&v)[8]) {
+  if (VEC) {
+    const int c = row_column<true>(i, 0, t, threads);
+    if (c < K) {
+      load8(row + c, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = fill;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = row_column<false>(i, j, t, threads);
+      v[j] = c < K ? to_f32(row[c]) : fill;
+    }
+  }
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_chunk(T* row, int K, int i, int t, int threads, const float (&v)[8]) {
+  if (VEC) {
+    const int c = row_column<true>(i, 0, t, threads);
+    if (c < K) store8(row + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = row_column<false>(i, j, t, threads);
+      if (c < K) row[c] = from_f32<T>(v[j]);
+    }
+  }
+}
+
+// A vector whose type is known at run time (svdq_dtype).
+template <bool VEC>
+__device__ __forceinline__ void load_param_chunk(const void* p, int dtype, size_t offset, int K, int i, int t,
+                                                 int threads, float fill, float (&v)[8]) {
+  if (dtype == SVDQ_DTYPE_BF16)
+    load_chunk<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(p) + offset, K, i, t, threads, fill, v);
+  else if (dtype == SVDQ_DTYPE_FP16)
+    load_chunk<__half, VEC>(static_cast<const __half*>(p) + offset, K, i, t, threads, fill, v);
+  else
+    load_chunk<float, VEC>(static_cast<const float*>(p) + offset, K, i, t, threads, fill, v);
+}
+
+// ------------------------------------------------------------- 8-bit checkpoint
+constexpr int kCkptGroup = 32;
+
+// The scale byte (exponent + 127) of a group from the bits of its largest magnitude: the smallest
+// power of two at which that magnitude does not leave the codes (int8: < 127.5, which rounds to
+// 127; E4M3: <= 448).  amax = m 2^k, so e = k - 6 (or k - 8), one more where m is at least
+// 127.5 / 64 (or above 448 / 256); e is at least -127 and, lest the largest code decode to an
+// infinity, at most that of k = 127.  0xFF for an infinity or a NaN.
+template <int FMT>
+__device__ __forceinline__ uint32_t ckpt_scale_byte(uint32_t amax_bits) {
+  if (amax_bits >= 0x7F800000u) return 0xFFu;
+  const int k = static_cast<int>(amax_bits >> 23);
+  const uint32_t m = amax_bits & 0x7FFFFFu;
+  const int b = FMT == SVDQ_CKPT8_INT8 ? k - 6 + (m >= 0x7F0000u) : k - 8 + (m > 0x600000u);
+  return static_cast<uint32_t>(min(max(b, 0), FMT == SVDQ_CKPT8_INT8 ? 248 : 246));
+}
+// 2^(byte - 127), exact (2^-127 is subnormal); NaN for 0xFF
+__device__ __forceinline__ float ckpt_scale(uint32_t byte) {
+  return byte == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte ? byte << 23 : 0x00400000u);
+}
+
+// Four codes of four values whose group has scale byte `byte`.  The product of an fp32 and a power
+// of two is exact here (where it is subnormal the code is 0 either way), so the code is the value
+// rounded once, ties to even.
+template <int FMT>
+__device__ __forceinline__ uint32_t ckpt_codes4(float a, float b, float c, float d, uint32_t byte) {
+  if (byte == 0xFFu) return 0u;  // a NaN or an infinity in the group
+  const float inv = __uint_as_float((254u - byte) << 23);
+  a *= inv, b *= inv, c *= inv, d *= inv;
+  if (FMT == SVDQ_CKPT8_INT8) {
+    if (byte == 248u) {  // the largest scale: magnitudes up to 128
+      a = fminf(fmaxf(a, -127.0f), 127.0f), b = fminf(fmaxf(b, -127.0f), 127.0f);
+      c = fminf(fmaxf(c, -127.0f), 127.0f), d = fminf(fmaxf(d, -127.0f), 127.0f);
+    }
+    const uint32_t lo = __byte_perm(__float2int_rn(a), __float2int_rn(b), 0x0040);
+    const uint32_t hi = __byte_perm(__float2int_rn(c), __float2int_rn(d), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
+  }
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
+}
+
+// Four codes as fp32, times their group's scale (exact).
+template <int FMT>
+__device__ __forceinline__ void ckpt_values4(uint32_t w, float scale, float* v) {
+  if (FMT == SVDQ_CKPT8_INT8) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = static_cast<float>(static_cast<int8_t>(w >> (8 * j))) * scale;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t h;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w >> (16 * j))));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      v[2 * j] = f.x * scale, v[2 * j + 1] = f.y * scale;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// Writes chunk i of a row's checkpoint: codes (K bytes) and scales (ceil(K / 32) bytes).  Every lane
+// of the warp calls it; columns beyond K hold 0.
+template <int FMT, bool VEC>
+__device__ __forceinline__ void ckpt_store_chunk(uint8_t* codes, uint8_t* scales, int K, int i, int t, int threads,
+                                                 const float (&v)[8]) {
+  if (VEC) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const uint32_t b = ckpt_scale_byte<FMT>(m);
+    const int c = row_column<true>(i, 0, t, threads);
+    if (c < K) {
+      *reinterpret_cast<uint2*>(codes + c) = make_uint2(ckpt_codes4<FMT>(v[0], v[1], v[2], v[3], b),
+                                                       ckpt_codes4<FMT>(v[4], v[5], v[6], v[7], b));
+      if (c % kCkptGroup == 0) scales[c / kCkptGroup] = static_cast<uint8_t>(b);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t b = ckpt_scale_byte<FMT>(__reduce_max_sync(0xffffffffu, abs_bits(v[j])));
+      const int c = row_column<false>(i, j, t, threads);
+      if (c < K) {
+        codes[c] = static_cast<uint8_t>(ckpt_codes4<FMT>(v[j], 0.0f, 0.0f, 0.0f, b) & 0xFFu);
+        if (c % kCkptGroup == 0) scales[c / kCkptGroup] = static_cast<uint8_t>(b);
+      }
+    }
+  }
+}
+
+// Chunk i of a row from its checkpoint; columns beyond K give 0.
+template <int FMT, bool VEC>
+__device__ __forceinline__ void ckpt_load_chunk(const uint8_t* codes, const uint8_t* scales, int K, int i, int t,
+                                                int threads, float (&v)[8]) {
+  if (VEC) {
+    const int c = row_column<true>(i, 0, t, threads);
+    if (c < K) {
+      const uint2 w = *reinterpret_cast<const uint2*>(codes + c);
+      const float s = ckpt_scale(scales[c / kCkptGroup]);
+      ckpt_values4<FMT>(w.x, s, v);
+      ckpt_values4<FMT>(w.y, s, v + 4);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = row_column<false>(i, j, t, threads);
+      float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (c < K) ckpt_values4<FMT>(codes[c], ckpt_scale(scales[c / kCkptGroup]), q);
+      v[j] = q[0];
+    }
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+}  // namespace dev
+}  // namespace svdq

@@ -133,6 +133,35 @@ svdq_status launch_gemm_int4(const GemmInt4Args& a, cudaStream_t stream);
 // and bf16 scales group-major [K/64][rows_pad] (padded rows left untouched).
 void int4_encode_rows(const float* R, int rows, int K, int rows_pad, uint8_t* codes, uint16_t* scales);
 
+// W4A16 layer for up to 16 tokens: workspace bytes and both kernels.
+size_t w4a16_workspace(int M, int K, int r_pad);
+svdq_status launch_w4a16(const svdq_weights* w, const void* X, int M, void* Y, void* workspace, cudaStream_t stream);
+
+// Layer norm and its gradient; strides in elements, `rows` per (scale, shift) vector (1 <= rows <= M).
+struct NormArgs {
+  int M, K, rows, dtype, param_dtype, plus_one;
+  float eps;
+  int64_t ld_z, ld_y, ld_dy, ld_dz, ld_param;
+};
+constexpr int kNormMaxK = 16384;
+svdq_status launch_layer_norm(const NormArgs& a, const void* Z, const void* scale, const void* shift, void* Y,
+                              float* stats, uint8_t* codes, uint8_t* scales, int ckpt, cudaStream_t stream);
+size_t layer_norm_backward_workspace(int M, int K, int rows);
+svdq_status launch_layer_norm_backward(const NormArgs& a, const void* dY, const void* Z, const uint8_t* codes,
+                                       const uint8_t* scales, int ckpt, const float* stats, const void* scale,
+                                       void* dZ, float* dscale, float* dshift, void* workspace, cudaStream_t stream);
+
+// 8-bit checkpoint of M rows of K values, `ld` elements apart.
+svdq_status launch_ckpt8_encode(const void* X, int dtype, int M, int K, int64_t ld, int format, uint8_t* codes,
+                                uint8_t* scales, cudaStream_t stream);
+svdq_status launch_ckpt8_decode(const uint8_t* codes, const uint8_t* scales, int M, int K, int format, void* X,
+                                int dtype, int64_t ld, cudaStream_t stream);
+
+// G[K, r] = X^T S; src 0: X is bf16 [M, K], 1 and 2: int8 and E4M3 codes with `scales`.
+size_t lowrank_wgrad_workspace(int M, int K, int r);
+svdq_status launch_lowrank_wgrad(const void* X, const uint8_t* scales, int src, const void* S, int M, int K, int r,
+                                 float* G, void* workspace, cudaStream_t stream);
+
 // Device self-test of the encoder's exact division and reciprocal shortcuts.
 svdq_status selftest_codec(unsigned int* mismatches_out);
 
