@@ -15,9 +15,11 @@ def __getattr__(name):
         return importlib.import_module(".build", __name__)
     binding = importlib.import_module(".binding", __name__)
     try:
-        return getattr(binding, name)
+        value = getattr(binding, name)
     except AttributeError:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}") from None
+    globals()[name] = value  # later lookups find it without this call
+    return value
 
 
 def __dir__():

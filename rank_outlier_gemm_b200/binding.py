@@ -10,6 +10,7 @@ fallback path, and importing this module fails if the library is not built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -158,56 +159,76 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _arg(t, name: str, shape, *dtypes) -> int:
+# The raw current stream of a device, without the Python object torch.cuda.current_stream() builds for it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _device_and_stream(stream) -> tuple:
+    """The current device and the raw stream to launch on (None: PyTorch's current stream there)."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2  # no tensor's device
+    if stream is not None:
+        return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if dev < 0:  # no CUDA tensor exists yet: the arguments' checks say so
+        return dev, None
+    return dev, _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _arg(t, name: str, shape, dtype, dev: int) -> int:
     """Address of a packed CUDA tensor of this shape and type on the current device."""
-    return _rows_arg(t, name, shape, dtypes, packed=True)[0]
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev and \
+            t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, shape, (dtype,), dev)
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _rows_arg(t, name: str, shape, dtypes, packed: bool = False) -> tuple:
-    """(address, elements between rows) of a CUDA tensor on the current device whose last index is
-    contiguous; `packed`: all of it is."""
+def _rows_arg(t, name: str, shape, dtypes, dev: int) -> tuple:
+    """(address, elements between rows) of a CUDA matrix on the current device whose last index is contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev):
+        _refuse(t, name, shape, dtypes, dev)
+    rows, cols = shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"the last index of {name} must be contiguous")
+    if rows <= 1:
+        ld = cols
+    elif ld < cols:
+        raise ValueError(f"the rows of {name} overlap")
+    return t.data_ptr(), ld
+
+
+def _refuse(t, name: str, shape, dtypes, dev: int) -> None:
+    """Raises ValueError with what is wrong with a tensor's kind, type, shape or device, if anything is."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has type {t.dtype}, not one of {', '.join(str(d) for d in dtypes)}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device {torch.cuda.current_device()}")
-    if packed:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr(), 0
-    rows, cols = shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"the last index of {name} must be contiguous")
-    ld = t.stride(0) if rows > 1 else cols
-    if ld < cols:
-        raise ValueError(f"the rows of {name} overlap")
-    return t.data_ptr(), ld
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on the current device {dev}")
 
 
-def _workspace(t: Optional[torch.Tensor]) -> tuple:
+def _workspace(t: Optional[torch.Tensor], dev: int) -> tuple:
     """(address, bytes) of a packed CUDA workspace, or of none."""
-    if t is None:
+    if t is None or t.numel() == 0:
         return None, 0
-    n = t.numel() * t.element_size()
-    return (_arg(t, "workspace", t.shape, t.dtype), n) if n else (None, 0)
+    return _arg(t, "workspace", t.shape, t.dtype, dev), t.numel() * t.element_size()
 
 
 def _shape2(t, name: str) -> tuple:
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
-    return tuple(t.shape)
+    return t.shape
 
 
-def _ckpt(ckpt, M: int, K: int) -> tuple:
+def _ckpt(ckpt, M: int, K: int, dev: int) -> tuple:
     """(codes, scales, format) arguments of a checkpoint (codes, scales, "int8" or "e4m3") or of none."""
     if ckpt is None:
         return None, None, 0
     codes, scales, fmt = ckpt
-    return (_arg(codes, "codes", (M, K), torch.uint8), _arg(scales, "scales", (M, (K + 31) // 32), torch.uint8),
-            _ckpt_format(fmt))
+    return (_arg(codes, "codes", (M, K), torch.uint8, dev),
+            _arg(scales, "scales", (M, (K + 31) // 32), torch.uint8, dev), _ckpt_format(fmt))
 
 
 def _ckpt_format(fmt: str) -> int:
@@ -381,34 +402,38 @@ def svdq_forward_norm_workspace_bytes(w: Weights, M: int) -> int:
 
 def svdq_linear_w4a16(w: Weights, X: torch.Tensor, Y: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """The layer on 1..16 tokens with 16-bit activations: X [M, K], Y [M, N], CUDA bf16."""
+    dev, s = _device_and_stream(stream)
     M, K = _shape2(X, "X")
-    ws, n = _workspace(workspace)
     if K != w.K:
         raise ValueError(f"X has {K} columns, the layer takes {w.K}")
-    _check(_lib.svdq_linear_w4a16(w.handle, _arg(X, "X", (M, K), torch.bfloat16), M,
-                                  _arg(Y, "Y", (M, w.N), torch.bfloat16), ws, n, _stream(stream)), "svdq_linear_w4a16")
+    ws, n = _workspace(workspace, dev)
+    st = _lib.svdq_linear_w4a16(w.handle, _arg(X, "X", (M, K), torch.bfloat16, dev), M,
+                                _arg(Y, "Y", (M, w.N), torch.bfloat16, dev), ws, n, s)
+    if st:
+        _check(st, "svdq_linear_w4a16")
 
 
 def svdq_linear_w4a16_workspace_bytes(w: Weights, M: int) -> int:
     return _lib.svdq_linear_w4a16_workspace_bytes(w.handle, M)
 
 
-def _norm_params(scale, shift, M: int, K: int, group_rows: int) -> tuple:
+def _norm_params(scale, shift, M: int, K: int, group_rows: int, dev: int) -> tuple:
     """(svdq_dtype, elements between groups, addresses) of the per-group vectors [groups, K]."""
-    groups = -(-M // (group_rows or M)) if M else 0
-    dtype, ld, ptrs = torch.float32, 0, []
-    for p, name in ((scale, "scale"), (shift, "shift")):
-        if p is None:
-            ptrs.append(None)
-            continue
-        if ptrs and ptrs[0] is not None and p.dtype != scale.dtype:
-            raise ValueError("scale and shift must have the same type")
-        at, stride = _rows_arg(p, name, (groups, K), DTYPES)
-        if ptrs and ptrs[0] is not None and stride != ld:
-            raise ValueError("scale and shift must have the same stride")
-        dtype, ld = p.dtype, stride
-        ptrs.append(at)
-    return DTYPES[dtype], ld, ptrs[0], ptrs[1]
+    shape = (-(-M // (group_rows or M)) if M else 0, K)
+    if scale is None and shift is None:
+        return 2, 0, None, None
+    sp, ld = _rows_arg(scale, "scale", shape, DTYPES, dev) if scale is not None else (None, 0)
+    if shift is None:
+        return DTYPES[scale.dtype], ld, sp, None
+    hp, ld_shift = _rows_arg(shift, "shift", shape, DTYPES, dev)
+    if sp is not None and (scale.dtype != shift.dtype or ld != ld_shift):
+        raise ValueError("scale and shift must have the same type and stride")
+    return DTYPES[shift.dtype], ld_shift, sp, hp
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_desc(*fields) -> NormDesc:
+    return NormDesc(*fields)
 
 
 def svdq_layer_norm(Z: torch.Tensor, scale: Optional[torch.Tensor], shift: Optional[torch.Tensor], Y: torch.Tensor,
@@ -420,14 +445,17 @@ def svdq_layer_norm(Z: torch.Tensor, scale: Optional[torch.Tensor], shift: Optio
     ckpt = (codes, scales, "int8" or "e4m3") also writes Z's 8-bit checkpoint (uint8 [M, K] and
     [M, ceil(K/32)]).
     """
+    dev, s = _device_and_stream(stream)
     M, K = _shape2(Z, "Z")
-    zp, ld_z = _rows_arg(Z, "Z", (M, K), DTYPES)
-    yp, ld_y = _rows_arg(Y, "Y", (M, K), (Z.dtype,))
-    pd, ld_p, sp, hp = _norm_params(scale, shift, M, K, group_rows)
-    d = NormDesc(M, K, group_rows, DTYPES[Z.dtype], pd, plus_one, eps, ld_z, ld_y, 0, 0, ld_p)
-    codes, scales, fmt = _ckpt(ckpt, M, K)
-    _check(_lib.svdq_layer_norm(d, zp, sp, hp, yp, _arg(stats, "stats", (M, 2), torch.float32) if stats is not None else None,
-                                codes, scales, fmt, _stream(stream)), "svdq_layer_norm")
+    zp, ld_z = _rows_arg(Z, "Z", (M, K), DTYPES, dev)
+    yp, ld_y = _rows_arg(Y, "Y", (M, K), (Z.dtype,), dev)
+    pd, ld_p, sp, hp = _norm_params(scale, shift, M, K, group_rows, dev)
+    stp = _arg(stats, "stats", (M, 2), torch.float32, dev) if stats is not None else None
+    codes, scales, fmt = _ckpt(ckpt, M, K, dev)
+    d = _norm_desc(M, K, group_rows, DTYPES[Z.dtype], pd, bool(plus_one), eps, ld_z, ld_y, 0, 0, ld_p)
+    st = _lib.svdq_layer_norm(d, zp, sp, hp, yp, stp, codes, scales, fmt, s)
+    if st:
+        _check(st, "svdq_layer_norm")
 
 
 def svdq_layer_norm_backward(dY: torch.Tensor, Z: Optional[torch.Tensor], stats: torch.Tensor,
@@ -435,19 +463,22 @@ def svdq_layer_norm_backward(dY: torch.Tensor, Z: Optional[torch.Tensor], stats:
                              dshift: Optional[torch.Tensor], workspace: Optional[torch.Tensor], group_rows: int = 0,
                              plus_one: bool = False, ckpt=None, stream=None) -> None:
     """Gradient of svdq_layer_norm from Z or (Z None) from its checkpoint; dscale and dshift float32 [groups, K]."""
+    dev, s = _device_and_stream(stream)
     M, K = _shape2(dY, "dY")
-    dyp, ld_dy = _rows_arg(dY, "dY", (M, K), DTYPES)
-    dzp, ld_dz = _rows_arg(dZ, "dZ", (M, K), (dY.dtype,))
-    zp, ld_z = _rows_arg(Z, "Z", (M, K), (dY.dtype,)) if Z is not None else (None, 0)
-    pd, ld_p, sp, _ = _norm_params(scale, None, M, K, group_rows)
-    groups = -(-M // (group_rows or M)) if M else 0
-    grads = [_arg(g, name, (groups, K), torch.float32) if g is not None else None
-             for g, name in ((dscale, "dscale"), (dshift, "dshift"))]
-    d = NormDesc(M, K, group_rows, DTYPES[dY.dtype], pd, plus_one, 0.0, ld_z, 0, ld_dy, ld_dz, ld_p)
-    codes, scales, fmt = _ckpt(ckpt, M, K)
-    ws, n = _workspace(workspace)
-    _check(_lib.svdq_layer_norm_backward(d, dyp, zp, codes, scales, fmt, _arg(stats, "stats", (M, 2), torch.float32), sp,
-                                         dzp, grads[0], grads[1], ws, n, _stream(stream)), "svdq_layer_norm_backward")
+    dyp, ld_dy = _rows_arg(dY, "dY", (M, K), DTYPES, dev)
+    dzp, ld_dz = _rows_arg(dZ, "dZ", (M, K), (dY.dtype,), dev)
+    zp, ld_z = _rows_arg(Z, "Z", (M, K), (dY.dtype,), dev) if Z is not None else (None, 0)
+    pd, ld_p, sp, _ = _norm_params(scale, None, M, K, group_rows, dev)
+    shape = (-(-M // (group_rows or M)) if M else 0, K)
+    da = _arg(dscale, "dscale", shape, torch.float32, dev) if dscale is not None else None
+    dc = _arg(dshift, "dshift", shape, torch.float32, dev) if dshift is not None else None
+    stp = _arg(stats, "stats", (M, 2), torch.float32, dev)
+    codes, scales, fmt = _ckpt(ckpt, M, K, dev)
+    ws, n = _workspace(workspace, dev)
+    d = _norm_desc(M, K, group_rows, DTYPES[dY.dtype], pd, bool(plus_one), 0.0, ld_z, 0, ld_dy, ld_dz, ld_p)
+    st = _lib.svdq_layer_norm_backward(d, dyp, zp, codes, scales, fmt, stp, sp, dzp, da, dc, ws, n, s)
+    if st:
+        _check(st, "svdq_layer_norm_backward")
 
 
 def svdq_layer_norm_backward_workspace_bytes(M: int, K: int, group_rows: int = 0) -> int:
@@ -457,31 +488,40 @@ def svdq_layer_norm_backward_workspace_bytes(M: int, K: int, group_rows: int = 0
 def svdq_ckpt8_encode(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, fmt: str = "int8",
                       stream=None) -> None:
     """8-bit checkpoint of a CUDA [M, K] tensor (bf16, fp16 or fp32) into uint8 [M, K] and [M, ceil(K/32)]."""
+    dev, s = _device_and_stream(stream)
     M, K = _shape2(X, "X")
-    xp, ld = _rows_arg(X, "X", (M, K), DTYPES)
-    cp, sp, f = _ckpt((codes, scales, fmt), M, K)
-    _check(_lib.svdq_ckpt8_encode(xp, DTYPES[X.dtype], M, K, ld, f, cp, sp, _stream(stream)), "svdq_ckpt8_encode")
+    xp, ld = _rows_arg(X, "X", (M, K), DTYPES, dev)
+    cp, sp, f = _ckpt((codes, scales, fmt), M, K, dev)
+    st = _lib.svdq_ckpt8_encode(xp, DTYPES[X.dtype], M, K, ld, f, cp, sp, s)
+    if st:
+        _check(st, "svdq_ckpt8_encode")
 
 
 def svdq_ckpt8_decode(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, fmt: str = "int8",
                       stream=None) -> None:
     """The values of a checkpoint into a CUDA [M, K] tensor (bf16, fp16 or fp32)."""
+    dev, s = _device_and_stream(stream)
     M, K = _shape2(X, "X")
-    xp, ld = _rows_arg(X, "X", (M, K), DTYPES)
-    cp, sp, f = _ckpt((codes, scales, fmt), M, K)
-    _check(_lib.svdq_ckpt8_decode(cp, sp, M, K, f, xp, DTYPES[X.dtype], ld, _stream(stream)), "svdq_ckpt8_decode")
+    xp, ld = _rows_arg(X, "X", (M, K), DTYPES, dev)
+    cp, sp, f = _ckpt((codes, scales, fmt), M, K, dev)
+    st = _lib.svdq_ckpt8_decode(cp, sp, M, K, f, xp, DTYPES[X.dtype], ld, s)
+    if st:
+        _check(st, "svdq_ckpt8_decode")
 
 
 def svdq_lowrank_wgrad(X: Optional[torch.Tensor], S: torch.Tensor, G: torch.Tensor, workspace: Optional[torch.Tensor],
                        ckpt=None, stream=None) -> None:
     """G [K, r] float32 = X^T S for CUDA bf16 X [M, K] (or, X None, its checkpoint) and S [M, r]."""
+    dev, s = _device_and_stream(stream)
     M, r = _shape2(S, "S")
     K = _shape2(G, "G")[0]
-    xp = _arg(X, "X", (M, K), torch.bfloat16) if X is not None else None
-    codes, scales, fmt = _ckpt(ckpt, M, K)
-    ws, n = _workspace(workspace)
-    _check(_lib.svdq_lowrank_wgrad(xp, codes, scales, fmt, _arg(S, "S", (M, r), torch.bfloat16), M, K, r,
-                                   _arg(G, "G", (K, r), torch.float32), ws, n, _stream(stream)), "svdq_lowrank_wgrad")
+    xp = _arg(X, "X", (M, K), torch.bfloat16, dev) if X is not None else None
+    codes, scales, fmt = _ckpt(ckpt, M, K, dev)
+    ws, n = _workspace(workspace, dev)
+    st = _lib.svdq_lowrank_wgrad(xp, codes, scales, fmt, _arg(S, "S", (M, r), torch.bfloat16, dev), M, K, r,
+                                 _arg(G, "G", (K, r), torch.float32, dev), ws, n, s)
+    if st:
+        _check(st, "svdq_lowrank_wgrad")
 
 
 def svdq_lowrank_wgrad_workspace_bytes(M: int, K: int, r: int) -> int:

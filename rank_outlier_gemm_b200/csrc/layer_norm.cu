@@ -10,8 +10,10 @@
 // fp32.  In the backward a thread keeps its columns over all rows that its CTA takes, so the column
 // sums stay in registers too; CTAs that share a group leave partial sums in the workspace and a
 // second kernel adds them in a fixed order (no atomics: equal calls give equal bits).
+#include <algorithm>
 #include <initializer_list>
 
+#include "ptx.cuh"
 #include "rows.cuh"
 #include "svdq_internal.h"
 
@@ -20,23 +22,38 @@ namespace {
 
 using namespace dev;
 
-constexpr int kTeamWarps = 8;  // warps of a CTA shared out to teams of up to that many
+// Warps of a CTA, shared out to teams (a team may have more: it is alone then).  The backward takes one CTA
+// of 16 warps per SM, which halves the partial sums that two of 8 would leave.
+constexpr int kForwardWarps = 8, kBackwardWarps = 16;
 
-// Sums of a and b over a team of `warps` warps, the same in every thread.  `red` holds two buffers
-// of 16 pairs per team, used in turn: the barrier of one call separates the reads of the call before
-// from the writes of the call after.
-__device__ __forceinline__ float2 team_sum2(float a, float b, int warps, int team, float2* red, int& turn) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if (warps == 1) return make_float2(a, b);
-  float2* r = red + turn * 16;
-  turn ^= 1;
-  const int w = (threadIdx.x >> 5) - team * warps;
-  if ((threadIdx.x & 31) == 0) r[w] = make_float2(a, b);
+// Sums over a team of `warps` warps, the same in every thread.  `red` holds two buffers of 2 x 16
+// values per team, used in turn: the barrier of one call separates the reads of the call before from
+// the writes of the call after.  Each warp adds the warps' values by shuffles, one value a lane.
+__device__ __forceinline__ void team_barrier(int team, int warps) {
   asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(warps * 32) : "memory");
-  float2 s = r[0];
-  for (int i = 1; i < warps; ++i) s.x += r[i].x, s.y += r[i].y;
-  return s;
+}
+// Of a and b: lanes 0-15 of the result hold the first sum, lanes 16-31 the second.
+__device__ __forceinline__ float team_sum_halves(float a, float b, int warps, int team, float* red, int& turn) {
+  float v = warp_sum2_halves(a, b);
+  if (warps == 1) return v;
+  const int lane = threadIdx.x & 31;
+  float* r = red + turn * 32;
+  turn ^= 1;
+  if ((lane & 15) == 0) r[lane + (threadIdx.x >> 5) - team * warps] = v;
+  team_barrier(team, warps);
+  v = (lane & 15) < warps ? r[lane] : 0.0f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float2 team_sum2(float a, float b, int warps, int team, float* red, int& turn) {
+  const float v = team_sum_halves(a, b, warps, team, red, turn);
+  const float o = __shfl_xor_sync(0xffffffffu, v, 16);
+  return (threadIdx.x & 16) ? make_float2(o, v) : make_float2(v, o);
+}
+__device__ __forceinline__ float team_sum(float a, int warps, int team, float* red, int& turn) {
+  if (warps == 1) return warp_sum(a);
+  return __shfl_sync(0xffffffffu, team_sum_halves(a, 0.0f, warps, team, red, turn), 0);
 }
 
 struct FwdParams {
@@ -54,7 +71,7 @@ struct FwdParams {
 
 template <typename T, int NV, bool VEC>
 __global__ void __launch_bounds__(512) layer_norm_kernel(FwdParams p) {
-  __shared__ float2 red[kTeamWarps][32];
+  __shared__ float red[kForwardWarps][64];
   const int threads = p.warps * 32, team = threadIdx.x / threads, t = threadIdx.x % threads;
   const int m = blockIdx.x * (blockDim.x / threads) + team;
   if (m >= p.M) return;  // whole teams: a barrier has all of its team's warps
@@ -80,7 +97,7 @@ __global__ void __launch_bounds__(512) layer_norm_kernel(FwdParams p) {
     }
   }
   const float inv_k = 1.0f / static_cast<float>(p.K);
-  const float mu = team_sum2(sum, 0.0f, p.warps, team, red[team], turn).x * inv_k;
+  const float mu = team_sum(sum, p.warps, team, red[team], turn) * inv_k;
   float sq = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -90,7 +107,7 @@ __global__ void __launch_bounds__(512) layer_norm_kernel(FwdParams p) {
       if (row_column<VEC>(i, j, t, threads) < p.K) sq = __fmaf_rn(v[i][j], v[i][j], sq);
     }
   }
-  const float var = team_sum2(sq, 0.0f, p.warps, team, red[team], turn).x * inv_k;
+  const float var = team_sum(sq, p.warps, team, red[team], turn) * inv_k;
   const float rstd = __frcp_rn(__fsqrt_rn(__fadd_rn(var, p.eps)));
   if (p.stats && t == 0) p.stats[m] = make_float2(mu, rstd);
   const size_t group = static_cast<size_t>(m / p.rows) * p.ld_param;
@@ -121,124 +138,331 @@ struct BwdParams {
   float* dshift;
   float* partial;         // [groups][splits][2][K], or null with one split
   int64_t ld_z, ld_dy, ld_dz, ld_param;
-  int M, K, rows, splits, param_dtype, warps;
+  int M, K, rows, splits, param_dtype, warps, teams, stages, packed;
   float one;
+  int* err;
+  uint64_t wait_ns;
+};
+
+constexpr int kMaxStages = 4;
+
+// A barrier of the CTA's `workers` threads (the copying warp is not among them).
+__device__ __forceinline__ void workers_barrier(int workers) { asm volatile("bar.sync 15, %0;" ::"r"(workers) : "memory"); }
+
+// Floats of the multipliers in shared memory: K, eight zeros, and 16-byte alignment behind them.
+__host__ __device__ constexpr int mul_floats(int K) { return (K + 8 + 3) / 4 * 4; }
+
+// A stage of the ring of the vector layout: one row for each of the CTA's teams, side by side (dY, then Z
+// or its codes), then the 4-byte aligned words that hold their scale bytes, then their statistics.
+template <typename T, int SRC>
+struct Stage {
+  int z, scales, stats, bytes;
+  __host__ __device__ Stage(int K, int teams)
+      : z(teams * K * static_cast<int>(sizeof(T))),
+        scales(z + teams * K * (SRC ? 1 : static_cast<int>(sizeof(T)))),
+        stats(scales + (SRC ? (teams * ((K + kCkptGroup - 1) / kCkptGroup) + 3 + 15) / 16 * 16 : 0)),
+        bytes(stats + (teams * 8 + 15) / 16 * 16) {}
 };
 
 // SRC: 0 the values themselves, 1 an int8 checkpoint, 2 an E4M3 one.
+// In the vector layout one more warp copies the teams' next rows, which are consecutive, into a ring of
+// `stages` stages in shared memory by bulk copies, so that memory stays busy across the rows'
+// reductions and the teams issue nothing for it.
 template <typename T, int NV, bool VEC, int SRC>
-__global__ void __launch_bounds__(512) layer_norm_backward_kernel(BwdParams p) {
-  extern __shared__ float sums[];  // [2][K] where several teams share the CTA
-  __shared__ float2 red[kTeamWarps][32];
-  const int threads = p.warps * 32, teams = blockDim.x / threads;
-  const int team = threadIdx.x / threads, t = threadIdx.x % threads;
+__global__ void __launch_bounds__(32 * (kBackwardWarps + 1)) layer_norm_backward_kernel(BwdParams p) {
+  // the multipliers, then the ring; at the end the teams' [2][K] sums where several share the CTA
+  extern __shared__ __align__(16) float smem[];
+  __shared__ float red[kBackwardWarps][64];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
+  __shared__ int s_abort;
+  constexpr int kFmt = SRC == 2 ? SVDQ_CKPT8_E4M3 : SVDQ_CKPT8_INT8;
+  // chunks of a row held across its reduction; with more than two the row is read again (in place: dZ may be
+  // dY, of which the element layout then holds what it overwrites)
+  constexpr int kHeld = NV <= 2 || !VEC ? NV : 1;
+  const int threads = p.warps * 32, teams = p.teams, workers = teams * threads;
+  const int team = threadIdx.x / threads, t = threadIdx.x % threads, lane = threadIdx.x & 31;
+  const Stage<T, SRC> at(p.K, teams);
   const int group = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
   const int first = group * p.rows, last = min(p.M, first + p.rows);
+  const int scale_row = (p.K + kCkptGroup - 1) / kCkptGroup;
   const float inv_k = 1.0f / static_cast<float>(p.K);
+  // the CTA's rows: `teams` consecutive ones from m0, m0 + step, ...
+  const int step = p.splits * teams, m0 = first + split * teams;
+  const WaitCtl ctl{p.err, p.wait_ns, &s_abort};
+  uint8_t* ring = reinterpret_cast<uint8_t*>(smem + mul_floats(p.K));
   int turn = 0;
 
-  float mul[NV][8], da[NV][8], dc[NV][8];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (p.scale)
-      load_param_chunk<VEC>(p.scale, p.param_dtype, static_cast<size_t>(group) * p.ld_param, p.K, i, t, threads, 0.0f,
-                            mul[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      mul[i][j] = p.scale ? mul[i][j] + p.one : 1.0f;
-      da[i][j] = dc[i][j] = 0.0f;
-    }
-  }
-
-  for (int m = first + split * teams + team; m < last; m += p.splits * teams) {
-    const float2 st = p.stats[m];
-    float x[NV][8], dy[NV][8];
-    float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      // beyond K: dy is 0, and so are its terms in every sum
-      load_chunk<T, VEC>(static_cast<const T*>(p.dY) + m * p.ld_dy, p.K, i, t, threads, 0.0f, dy[i]);
-      if (SRC == 0)
-        load_chunk<T, VEC>(static_cast<const T*>(p.Z) + m * p.ld_z, p.K, i, t, threads, 0.0f, x[i]);
-      else
-        ckpt_load_chunk<SRC == 1 ? SVDQ_CKPT8_INT8 : SVDQ_CKPT8_E4M3, VEC>(
-            p.codes + static_cast<size_t>(m) * p.K,
-            p.scales + static_cast<size_t>(m) * ((p.K + kCkptGroup - 1) / kCkptGroup), p.K, i, t, threads, x[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        // a row that is not finite gives NaN statistics: its padding must not reach the sums
-        const bool in = row_column<VEC>(i, j, t, threads) < p.K;
-        x[i][j] = in ? (x[i][j] - st.x) * st.y : 0.0f;
-        da[i][j] = __fmaf_rn(dy[i][j], x[i][j], da[i][j]);
-        dc[i][j] += dy[i][j];
-        dy[i][j] *= in ? mul[i][j] : 0.0f;
-        s1 += dy[i][j];
-        s2 = __fmaf_rn(dy[i][j], x[i][j], s2);
+  if (VEC) {
+    if (threadIdx.x == 0) {
+      s_abort = 0;
+      for (int s = 0; s < p.stages; ++s) {
+        mbar_init(&full[s], 33);
+        mbar_init(&empty[s], workers / 32);
       }
+      fence_barrier_init();
     }
-    const float2 s = team_sum2(s1, s2, p.warps, team, red[team], turn);
-    const float m1 = s.x * inv_k, m2 = s.y * inv_k;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) dy[i][j] = st.y * (dy[i][j] - m1 - x[i][j] * m2);
-      store_chunk<T, VEC>(static_cast<T*>(p.dZ) + m * p.ld_dz, p.K, i, t, threads, dy[i]);
-    }
-  }
-
-  float* out_a = p.partial ? p.partial + static_cast<size_t>(blockIdx.x) * 2 * p.K
-                           : p.dscale ? p.dscale + static_cast<size_t>(group) * p.K : nullptr;
-  float* out_c = p.partial ? out_a + p.K : p.dshift ? p.dshift + static_cast<size_t>(group) * p.K : nullptr;
-  if (teams > 1) {  // the teams add their columns in turn
-    for (int r = 0; r < teams; ++r) {
-      if (team == r) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int c = row_column<VEC>(i, j, t, threads);
-            if (c < p.K) {
-              sums[c] = r ? sums[c] + da[i][j] : da[i][j];
-              sums[p.K + c] = r ? sums[p.K + c] + dc[i][j] : dc[i][j];
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) >= workers) {
+      uint32_t parity = 1;  // of the stage's release; the first pass finds every stage free
+      int stage = 0;
+      for (int m = m0; m < last; m += step) {
+        if (!wait_warp(&empty[stage], parity, ctl)) break;
+        const int n = min(teams, last - m);
+        uint64_t* bar = &full[stage];
+        uint8_t* to = ring + stage * at.bytes;
+        const uint32_t dy = p.K * sizeof(T), z = SRC ? p.K : p.K * sizeof(T);
+        if (lane == 0) mbar_arrive_expect_tx(bar, n * (dy + z));
+        __syncwarp();
+        if (p.packed) {
+          if (lane == 0) bulk_load(to, static_cast<const T*>(p.dY) + m * p.ld_dy, n * dy, bar);
+          if (lane == 1)
+            bulk_load(to + at.z, SRC ? static_cast<const void*>(p.codes + static_cast<size_t>(m) * p.K)
+                                     : static_cast<const T*>(p.Z) + m * p.ld_z, n * z, bar);
+        } else if (lane < n) {
+          bulk_load(to + lane * dy, static_cast<const T*>(p.dY) + (m + lane) * p.ld_dy, dy, bar);
+          bulk_load(to + at.z + lane * z, SRC ? static_cast<const void*>(p.codes + static_cast<size_t>(m + lane) * p.K)
+                                              : static_cast<const T*>(p.Z) + (m + lane) * p.ld_z, z, bar);
+        }
+        if (lane < n) copy8_async(to + at.stats + lane * 8, p.stats + m + lane);
+        if (SRC) {
+          const uint8_t* from = p.scales + static_cast<size_t>(m) * scale_row;
+          const uint8_t* base = from - (reinterpret_cast<uintptr_t>(from) & 3);
+          const uint8_t* end = p.scales + static_cast<size_t>(p.M) * scale_row;
+          const int words = static_cast<int>(from + n * scale_row - base + 3) / 4;
+          for (int i = lane; i < words; i += 32) {
+            const uint8_t* word = base + 4 * i;
+            if (word >= p.scales && word + 4 <= end) {
+              copy4_async(to + at.scales + 4 * i, word);
+            } else {  // the array's first or last bytes
+              for (int b = 0; b < 4; ++b)
+                if (word + b >= p.scales && word + b < end) to[at.scales + 4 * i + b] = word[b];
+              __threadfence_block();
             }
           }
         }
+        copies_arrive(bar);
+        if (++stage == p.stages) stage = 0, parity ^= 1;
       }
-      __syncthreads();
+      return;
     }
-    for (int c = threadIdx.x; c < p.K; c += blockDim.x) {
-      if (out_a) out_a[c] = sums[c];
-      if (out_c) out_c[c] = sums[p.K + c];
+  }
+
+  float* mul = smem;
+  if (team == 0) {
+    float w[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[i][j] = 1.0f - p.one;
+      if (p.scale)
+        load_param_chunk<VEC>(p.scale, p.param_dtype, static_cast<size_t>(group) * p.ld_param, p.K, i, t, threads, 0.0f,
+                              w[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[i][j] += p.one;
+      store_chunk<float, VEC>(mul, p.K, i, t, threads, w[i]);
+    }
+    if (t < 8) mul[p.K + t] = 0.0f;
+  }
+  workers_barrier(workers);
+
+  F2 da[NV][4], dc[NV][4];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) da[i][j] = dc[i][j] = f2(0.0f, 0.0f);
+
+  // a chunk beyond K works on column 0 with multipliers 0: it adds nothing to the row's sums and its own are dropped
+  int col[NV], mcol[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c0 = row_column<true>(i, 0, t, threads);
+    col[i] = c0 < p.K ? c0 : 0;
+    mcol[i] = c0 < p.K ? c0 : p.K;
+  }
+  uint32_t parity = 0;
+  int stage = 0;
+  bool alive = true;  // false once a wait ran out: the error word says so, the results are garbage
+  for (int m = m0 + team, block = m0; block < last; block += step, m += step) {
+    const uint8_t* here = ring + stage * at.bytes;
+    if (VEC) alive = wait_warp(&full[stage], parity, ctl) && alive;
+    if (m < last) {
+      F2 x[kHeld][4], g[kHeld][4];
+      F2 s1 = f2(0.0f, 0.0f), s2 = s1;
+      const float2 st = VEC ? *reinterpret_cast<const float2*>(here + at.stats + team * 8) : __ldg(p.stats + m);
+      const T* row_dy = reinterpret_cast<const T*>(here) + team * p.K;
+      const uint8_t* row_z = here + at.z + team * p.K * (SRC ? 1 : sizeof(T));
+      const uint8_t* row_s = here + at.scales + team * scale_row +
+                             ((static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.scales)) +
+                               static_cast<uint32_t>(block) * static_cast<uint32_t>(scale_row)) & 3);
+      const float rstd = st.y, shift = -st.x * rstd;  // xh = z rstd - mu rstd
+      // chunk i: dy, xh and the multipliers
+      auto read = [&](int i, F2(&d)[4], F2(&xh)[4], F2(&w)[4]) {
+        float mult = rstd;
+        if (VEC) {
+          const int c0 = col[i];
+          load8_pairs(row_dy + c0, d);
+          if (SRC) {  // the scale, a power of two, goes into the multiplier
+            ckpt_codes8_pairs<kFmt>(*reinterpret_cast<const uint2*>(row_z + c0), xh);
+            mult *= ckpt_scale(row_s[static_cast<uint32_t>(c0) / kCkptGroup]);
+          } else {
+            load8_pairs(reinterpret_cast<const T*>(row_z) + c0, xh);
+          }
+          load8_pairs(mul + mcol[i], w);
+        } else {
+          float a[8], b[8], c[8];
+          load_chunk<T, false>(static_cast<const T*>(p.dY) + m * p.ld_dy, p.K, i, t, threads, 0.0f, a);
+          if (SRC == 0)
+            load_chunk<T, false>(static_cast<const T*>(p.Z) + m * p.ld_z, p.K, i, t, threads, 0.0f, b);
+          else
+            ckpt_load_chunk<kFmt, false>(p.codes + static_cast<size_t>(m) * p.K,
+                                         p.scales + static_cast<size_t>(m) * scale_row, p.K, i, t, threads, b);
+          load_chunk<float, false>(mul, p.K, i, t, threads, 0.0f, c);  // columns beyond K: g = 0
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            d[j] = f2(a[2 * j], a[2 * j + 1]);
+            xh[j] = f2(b[2 * j], b[2 * j + 1]);
+            w[j] = f2(c[2 * j], c[2 * j + 1]);
+          }
+        }
+        const F2 scaled = f2(mult, mult), off = f2(shift, shift);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xh[j] = fma2(xh[j], scaled, off);
+      };
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        F2(&xh)[4] = x[kHeld == NV ? i : 0];
+        F2(&gi)[4] = g[kHeld == NV ? i : 0];
+        F2 w[4];
+        read(i, gi, xh, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          da[i][j] = fma2(gi[j], xh[j], da[i][j]);
+          dc[i][j] = add2(dc[i][j], gi[j]);
+          gi[j] = mul2(gi[j], w[j]);
+          s1 = add2(s1, gi[j]);
+          s2 = fma2(gi[j], xh[j], s2);
+        }
+      }
+      float a1, b1, a2, b2;
+      unpack2(s1, a1, b1);
+      unpack2(s2, a2, b2);
+      if (VEC && kHeld == NV) {  // the row is in registers
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+      }
+      const float2 s = team_sum2(a1 + b1, a2 + b2, p.warps, team, red[team], turn);
+      const F2 m1 = f2(-s.x * inv_k, -s.x * inv_k), m2 = f2(-s.y * inv_k, -s.y * inv_k), rs = f2(rstd, rstd);
+      T* dz = static_cast<T*>(p.dZ) + m * p.ld_dz;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        F2(&xh)[4] = x[kHeld == NV ? i : 0];
+        F2(&gi)[4] = g[kHeld == NV ? i : 0];
+        if (kHeld != NV) {
+          F2 w[4];
+          read(i, gi, xh, w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) gi[j] = mul2(gi[j], w[j]);
+        }
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) unpack2(mul2(rs, fma2(xh[j], m2, add2(gi[j], m1))), v[2 * j], v[2 * j + 1]);
+        store_chunk<T, VEC>(dz, p.K, i, t, threads, v);
+      }
+      if (VEC && kHeld != NV) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+      }
+    } else if (VEC && lane == 0) {
+      mbar_arrive(&empty[stage]);
+    }
+    if (++stage == p.stages) stage = 0, parity ^= 1;
+  }
+  // after a wait that ran out, nothing may still be on its way when the CTA ends
+  if (VEC && threadIdx.x == 0 && s_abort) {
+    WaitCtl drain = ctl;
+    int none = 0;
+    drain.abort = &none;
+    for (int s = 0; s < p.stages; ++s) wait_bounded(&full[s], s < stage ? parity : parity ^ 1, drain);
+  }
+
+  float fa[NV][8], fc[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      unpack2(da[i][j], fa[i][2 * j], fa[i][2 * j + 1]);
+      unpack2(dc[i][j], fc[i][2 * j], fc[i][2 * j + 1]);
+    }
+  grid_dep_launch_dependents();  // the joining kernel may be put in place
+  float* out_a = p.partial ? p.partial + static_cast<size_t>(blockIdx.x) * 2 * p.K
+                           : p.dscale ? p.dscale + static_cast<size_t>(group) * p.K : nullptr;
+  float* out_c = p.partial ? out_a + p.K : p.dshift ? p.dshift + static_cast<size_t>(group) * p.K : nullptr;
+  if (teams > 1) {  // the teams' sums side by side, then added in order
+    float* sums = smem;  // [teams][2][K]
+    workers_barrier(workers);  // the multipliers and the ring are done with
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      store_chunk<float, VEC>(sums + team * 2 * p.K, p.K, i, t, threads, fa[i]);
+      store_chunk<float, VEC>(sums + (team * 2 + 1) * p.K, p.K, i, t, threads, fc[i]);
+    }
+    workers_barrier(workers);
+    constexpr int kWide = VEC ? 4 : 1;
+    for (int c = threadIdx.x * kWide; c < 2 * p.K; c += workers * kWide) {
+      float s[kWide];
+#pragma unroll
+      for (int j = 0; j < kWide; ++j) s[j] = sums[c + j];
+      for (int r = 1; r < teams; ++r)
+#pragma unroll
+        for (int j = 0; j < kWide; ++j) s[j] += sums[r * 2 * p.K + c + j];
+      float* out = c < p.K ? out_a + c : out_c + (c - p.K);
+      if (c < p.K ? out_a : out_c)
+#pragma unroll
+        for (int j = 0; j < kWide; ++j) out[j] = s[j];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (out_a) store_chunk<float, VEC>(out_a, p.K, i, t, threads, da[i]);
-      if (out_c) store_chunk<float, VEC>(out_c, p.K, i, t, threads, dc[i]);
+      if (out_a) store_chunk<float, VEC>(out_a, p.K, i, t, threads, fa[i]);
+      if (out_c) store_chunk<float, VEC>(out_c, p.K, i, t, threads, fc[i]);
     }
   }
 }
 
-// dscale and dshift from the partial sums: 32 columns and 8 shares of the splits per CTA.
-__global__ void __launch_bounds__(256) layer_norm_sum_kernel(const float* __restrict__ partial, int splits, int K,
-                                                          float* dscale, float* dshift) {
-  __shared__ float part[8][32];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), share = threadIdx.x >> 5, group = blockIdx.y, which = blockIdx.z;
+// dscale and dshift from the partial sums: 32 columns per CTA, its warps share the splits out.
+// Launched while the first kernel still runs; the wait is for its results.
+constexpr int kMaxSplits = 148;  // one CTA per SM
+__global__ void __launch_bounds__(1024) layer_norm_sum_kernel(const float* __restrict__ partial, int splits, int K,
+                                                           float* dscale, float* dshift) {
+  __shared__ float part[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int c = blockIdx.x * 32 + lane, group = blockIdx.y, which = blockIdx.z;
   float* out = which ? dshift : dscale;
+  grid_dep_wait();
   if (!out) return;
+  const size_t pitch = static_cast<size_t>(2) * K;
+  const float* from = partial + static_cast<size_t>(group) * splits * pitch + static_cast<size_t>(which) * K + c;
   float s = 0.0f;
-  if (c < K)
-    for (int i = share; i < splits; i += 8)
-      s += partial[((static_cast<size_t>(group) * splits + i) * 2 + which) * K + c];
-  part[share][threadIdx.x & 31] = s;
+  if (c < K) {
+    for (int i = warp; i < splits; i += 5 * warps) {  // five loads in flight
+      float v[5];
+#pragma unroll
+      for (int j = 0; j < 5; ++j) v[j] = i + j * warps < splits ? __ldg(from + (i + j * warps) * pitch) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 5; ++j) s += v[j];
+    }
+  }
+  part[warp][lane] = s;
   __syncthreads();
-  if (share == 0 && c < K) {
-    for (int i = 1; i < 8; ++i) s += part[i][threadIdx.x];
+  if (warp == 0 && c < K) {
+    for (int i = 1; i < warps; ++i) s += part[i][lane];
     out[static_cast<size_t>(group) * K + c] = s;
   }
 }
 
-constexpr int kSMs = 148;
+constexpr int kMaxSmem = 220 * 1024;
 
 struct Shape {
   int nv, warps, teams;
@@ -259,24 +483,25 @@ Shape forward_shape(int K) {
       if (warps <= 16 && warps * nv < best) best = warps * nv, s.nv = nv, s.warps = warps;
     }
   }
-  s.teams = s.warps >= kTeamWarps ? 1 : kTeamWarps / s.warps;
+  s.teams = s.warps >= kForwardWarps ? 1 : kForwardWarps / s.warps;
   return s;
 }
 
-// Backward: 24 fp32 a chunk stay in registers over all rows, so as few chunks as 16 warps allow.
+// Backward: 16 sums a chunk stay in registers over all rows and 16 more values across a row's reduction:
+// two chunks a thread while 16 warps reach, then three or four.
 Shape backward_shape(int K) {
   const int nvec = (K + 7) / 8;
   Shape s{};
-  s.nv = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
+  s.nv = nvec <= 32 ? 1 : nvec <= 1024 ? 2 : nvec <= 1536 ? 3 : 4;
   s.warps = (nvec + 32 * s.nv - 1) / (32 * s.nv);
-  s.teams = s.warps >= kTeamWarps ? 1 : kTeamWarps / s.warps;
+  s.teams = s.warps >= kBackwardWarps ? 1 : kBackwardWarps / s.warps;
   return s;
 }
 
-// CTAs that share a group's rows: two per SM over all groups, four rows a team at least.
+// CTAs that share a group's rows: one per SM over all groups, four rows a team at least.
 int backward_splits(int K, int rows, int groups) {
   const Shape s = backward_shape(K);
-  const int want = (2 * kSMs + groups - 1) / groups;
+  const int want = (kMaxSplits + groups - 1) / groups;  // at most kMaxSplits
   const int most = (rows + 4 * s.teams - 1) / (4 * s.teams);
   return want < most ? want : most;
 }
@@ -301,9 +526,25 @@ svdq_status forward_nv(const FwdParams& p, const Shape& s, cudaStream_t stream) 
 }
 
 template <typename T, int NV, bool VEC, int SRC>
-svdq_status run_backward(const BwdParams& p, const Shape& s, int groups, cudaStream_t stream) {
-  const size_t smem = s.teams > 1 ? static_cast<size_t>(p.K) * 8 : 0;  // teams > 1: K <= 4096, 32 KB at most
-  layer_norm_backward_kernel<T, NV, VEC, SRC><<<groups * p.splits, s.teams * s.warps * 32, smem, stream>>>(p);
+svdq_status run_backward(BwdParams p, const Shape& s, int groups, cudaStream_t stream) {
+  const size_t mul = mul_floats(p.K) * sizeof(float);
+  const size_t sums = s.teams > 1 ? static_cast<size_t>(s.teams) * p.K * 8 : 0;  // 16 KB a warp at most
+  const size_t stage = Stage<T, SRC>(p.K, s.teams).bytes;
+  size_t smem = mul;
+  if (VEC) {  // up to four rows in flight per team
+    p.packed = p.ld_dy == p.K && (SRC || p.ld_z == p.K);
+    p.stages = kMaxStages;
+    while (p.stages > 1 && mul + p.stages * stage > kMaxSmem) --p.stages;
+    smem += p.stages * stage;
+  }
+  if (smem < sums) smem = sums;
+  p.err = device_error_word();
+  if (!p.err) return fail(SVDQ_ERR_CUDA, "device error word unavailable");
+  p.wait_ns = wait_limit_ns();
+  auto* kernel = layer_norm_backward_kernel<T, NV, VEC, SRC>;
+  if (smem > 40 * 1024)  // beside the static arrays
+    SVDQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem));
+  kernel<<<groups * p.splits, (s.teams * s.warps + (VEC ? 1 : 0)) * 32, smem, stream>>>(p);
   SVDQ_CUDA_TRY(cudaGetLastError());
   return SVDQ_OK;
 }
@@ -313,6 +554,7 @@ svdq_status backward_nv(const BwdParams& p, const Shape& s, int groups, cudaStre
   switch (s.nv) {
     case 1: return run_backward<T, 1, VEC, SRC>(p, s, groups, stream);
     case 2: return run_backward<T, 2, VEC, SRC>(p, s, groups, stream);
+    case 3: return run_backward<T, 3, VEC, SRC>(p, s, groups, stream);
     default: return run_backward<T, 4, VEC, SRC>(p, s, groups, stream);
   }
 }
@@ -367,10 +609,11 @@ svdq_status launch_layer_norm_backward(const NormArgs& a, const void* dY, const 
   const Shape s = backward_shape(a.K);
   BwdParams p{dY, Z, codes, scales, reinterpret_cast<const float2*>(stats), scale, dZ, dscale, dshift, nullptr,
               a.ld_z, a.ld_dy, a.ld_dz, a.ld_param, a.M, a.K, a.rows, backward_splits(a.K, a.rows, groups),
-              a.param_dtype, s.warps, a.plus_one ? 1.0f : 0.0f};
+              a.param_dtype, s.warps, s.teams, 0, 0, a.plus_one ? 1.0f : 0.0f, nullptr, 0};
   if (p.splits > 1 && (dscale || dshift)) p.partial = static_cast<float*>(workspace);
   const bool vec = vector_rows(a.K, {dY, Z, codes, scale, dZ, p.partial ? nullptr : dscale, p.partial ? nullptr : dshift},
-                               {a.ld_z, a.ld_dy, a.ld_dz, a.ld_param});
+                               {a.ld_z, a.ld_dy, a.ld_dz, a.ld_param}) &&
+                   (!codes || a.K % 16 == 0);  // bulk copies of whole rows of codes
   const int src = !codes ? 0 : ckpt == SVDQ_CKPT8_INT8 ? 1 : 2;
   svdq_status st;
   switch (a.dtype) {
@@ -380,8 +623,17 @@ svdq_status launch_layer_norm_backward(const NormArgs& a, const void* dY, const 
   }
   SVDQ_TRY(st);
   if (p.partial) {
-    layer_norm_sum_kernel<<<dim3((a.K + 31) / 32, groups, 2), 256, 0, stream>>>(p.partial, p.splits, a.K, dscale, dshift);
-    SVDQ_CUDA_TRY(cudaGetLastError());
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((a.K + 31) / 32, groups, 2);
+    cfg.blockDim = dim3(32 * std::min(32, std::max(1, (p.splits + 4) / 5)));  // five splits a warp
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    SVDQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, layer_norm_sum_kernel, static_cast<const float*>(p.partial), p.splits, a.K,
+                                     dscale, dshift));
   }
   return SVDQ_OK;
 }

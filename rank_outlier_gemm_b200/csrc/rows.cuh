@@ -81,6 +81,47 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+// Two fp32 in a register pair: one instruction works on both (sm_100 add, mul and fma .f32x2).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(F2 a, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// Eight values in shared or global memory as four pairs.
+__device__ __forceinline__ void load8_pairs(const float* p, F2 (&v)[4]) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(p), b = *reinterpret_cast<const ulonglong2*>(p + 4);
+  v[0].v = a.x, v[1].v = a.y, v[2].v = b.x, v[3].v = b.y;
+}
+template <typename T>
+__device__ __forceinline__ void load8_pairs(const T* p, F2 (&v)[4]) {
+  float f[8];
+  load8(p, f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = f2(f[2 * j], f[2 * j + 1]);
+}
+
 // Column of value j of chunk i of thread t.
 template <bool VEC>
 __device__ __forceinline__ int row_column(int i, int j, int t, int threads) {
@@ -181,7 +222,9 @@ template <int FMT>
 __device__ __forceinline__ void ckpt_values4(uint32_t w, float scale, float* v) {
   if (FMT == SVDQ_CKPT8_INT8) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = static_cast<float>(static_cast<int8_t>(w >> (8 * j))) * scale;
+    // q + 128 in the low mantissa bits of 2^23, less 2^23 + 128: exact, and no conversion instruction
+    for (int j = 0; j < 4; ++j)
+      v[j] = (__uint_as_float(__byte_perm(w ^ 0x80808080u, 0x4B000000u, 0x7540 + j)) - 8388736.0f) * scale;
   } else {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -189,6 +232,26 @@ __device__ __forceinline__ void ckpt_values4(uint32_t w, float scale, float* v) 
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w >> (16 * j))));
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
       v[2 * j] = f.x * scale, v[2 * j + 1] = f.y * scale;
+    }
+  }
+}
+
+// Eight codes as four pairs, not yet times their group's scale (exact).
+template <int FMT>
+__device__ __forceinline__ void ckpt_codes8_pairs(uint2 q, F2 (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t w = j < 2 ? q.x : q.y;
+    if (FMT == SVDQ_CKPT8_INT8) {
+      const uint32_t u = w ^ 0x80808080u;
+      const F2 b = f2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540 + 2 * (j & 1))),
+                      __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7541 + 2 * (j & 1))));
+      v[j] = add2(b, f2(-8388736.0f, -8388736.0f));
+    } else {
+      uint32_t h;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w >> (16 * (j & 1)))));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      v[j] = f2(f.x, f.y);
     }
   }
 }
@@ -250,6 +313,17 @@ __device__ __forceinline__ void ckpt_load_chunk(const uint8_t* codes, const uint
       v[j] = q[0];
     }
   }
+}
+
+// Sums of a and b over the warp with 5 + 1 shuffles instead of 10: the halves take one value each.
+// Lanes 0-15 get the first, lanes 16-31 the second.
+__device__ __forceinline__ float warp_sum2_halves(float a, float b) {
+  const bool upper = threadIdx.x & 16;
+  const float other = __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+  float v = (upper ? b : a) + other;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
