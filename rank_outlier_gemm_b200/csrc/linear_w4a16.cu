@@ -20,6 +20,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "ptx.cuh"
 #include "rows.cuh"
 #include "svdq_internal.h"
 
@@ -28,13 +29,14 @@ namespace {
 
 using namespace dev;
 
+constexpr int kSMs = 148;
 constexpr int kMaxTokens = 16;
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kPrepWarps = 16, kPrepThreads = 32 * kPrepWarps;
 constexpr int kStep = 128;        // weights of a row per warp step: 4 lanes x 32
-constexpr int kUnitRows = 32;     // weight rows per CTA: two M = 16 tiles
-constexpr int kTWarpK = 128;      // k per warp of the T kernel part
-constexpr int kTSplit = kTWarpK * kWarps;
+constexpr int kUnitRows = 32;     // weight rows per warp: two M = 16 tiles
+constexpr int kSlices = 2, kGroups = 4, kWarps = kSlices * kGroups;  // of a CTA: units, and warps per unit
+constexpr int kTWarpK = 64;       // k per warp in a split of T
+constexpr int kTSplit = kTWarpK * kPrepWarps;
 
 struct W4A16Params {
   const uint16_t* X;      // bf16 [M, K]
@@ -49,6 +51,7 @@ struct W4A16Params {
   float* pow2;            // [M] the tokens' scales
   float* T;               // [splits of K][M][r_pad]
   int M, N, K, r_pad, steps, tiles, t_splits;
+  int groups, cluster, blocks;  // of steps; CTAs that share an output; pairs of units
   float alpha_w;
 };
 
@@ -71,6 +74,19 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// What rounding to `hi` left of v; nothing of an infinity or a NaN, which stays in hi alone.
+__device__ __forceinline__ float rest(float v, float hi) { return isfinite(hi) ? v - hi : 0.0f; }
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
 
 // Eight E2M1 codes of a word (low nibble first) as four fp16 pairs.
 __device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&h)[4]) {
@@ -104,47 +120,56 @@ __device__ __forceinline__ int unit_row(int u, int b, int g) {
 
 // CTAs 0..M-1: a token's columns and scale.  The others: 16 ranks of T over one split of K.
 template <bool INT4>
-__global__ void __launch_bounds__(kThreads) w4a16_prepare_kernel(W4A16Params p) {
-  __shared__ float red[kWarps][16][16];
+__global__ void __launch_bounds__(kPrepThreads) w4a16_prepare_kernel(W4A16Params p) {
+  __shared__ float red[kPrepWarps][16][16];
+  grid_dep_launch_dependents();  // the second kernel starts on the weights
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   if (static_cast<int>(blockIdx.x) < p.M) {
     const int m = blockIdx.x;
     const uint16_t* x = p.X + static_cast<size_t>(m) * p.K;
-    auto chunk = [&](int c, float (&v)[8]) {  // xh of columns 8 c..8 c + 7, 0 beyond K
+    // xh of columns 8 c..8 c + 7, 0 beyond K; the first kHeld chunks of a thread stay in registers
+    constexpr int kHeld = 4;
+    auto chunk = [&](int c, float (&v)[8]) {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      float f[8] = {};
       if (c * 8 < p.K) {
-        float f[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(x) + c), v, static_cast<const __nv_bfloat16*>(nullptr));
+        w = __ldg(reinterpret_cast<const uint4*>(x) + c);
         load8(p.inv_lam + c * 8, f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= f[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
       }
+      unpack8(w, v, static_cast<const __nv_bfloat16*>(nullptr));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= f[j];
     };
+    const int chunks = p.steps * (kStep / 8);
     uint32_t top = 0;  // bits of the largest finite magnitude
-    for (int c = threadIdx.x; c < p.K / 8; c += kThreads) {
-      float v[8];
-      chunk(c, v);
+    auto note = [&](const float (&v)[8]) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t a = abs_bits(v[j]);
         if (a < 0x7F800000u) top = max(top, a);
       }
+    };
+    float held[kHeld][8];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) chunk(threadIdx.x + i * kPrepThreads, held[i]);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) note(held[i]);
+    for (int c = threadIdx.x + kHeld * kPrepThreads; c < chunks; c += kPrepThreads) {
+      float v[8];
+      chunk(c, v);
+      note(v);
     }
     top = __reduce_max_sync(0xffffffffu, top);
     uint32_t* r = reinterpret_cast<uint32_t*>(red);
     if (lane == 0) r[warp] = top;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = max(top, r[w]);
+    top = __reduce_max_sync(0xffffffffu, lane < kPrepWarps ? r[lane] : 0u);
     const int e = max(static_cast<int>(top >> 23) - 13, 1);  // biased: the scale is 2^(e - 127), a normal number
     const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
     if (threadIdx.x == 0) p.pow2[m] = __uint_as_float(static_cast<uint32_t>(e) << 23);
-    for (int c = threadIdx.x; c < p.steps * (kStep / 8); c += kThreads) {
-      float v[8];
-      chunk(c, v);
+    auto place = [&](int c, const float (&v)[8]) {
+      if (c >= chunks) return;
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -152,16 +177,23 @@ __global__ void __launch_bounds__(kThreads) w4a16_prepare_kernel(W4A16Params p) 
         const __half2 h = __floats2half2_rn(a, b);
         const float2 f = __half22float2(h);
         // an infinity or a NaN stays in hi alone
-        const float la = isfinite(a) ? a - f.x : 0.0f, lb = isfinite(b) ? b - f.y : 0.0f;
+        const float la = rest(a, f.x), lb = rest(b, f.y);
         hi[j] = as_u32(h);
         lo[j] = as_u32(__floats2half2_rn(la, lb));
       }
       const int w = c % 16;  // place in the 128-wide step
       const int q = INT4 ? (w >> 3) * 2 + (w & 1) : w & 3, ft = INT4 ? (w & 7) >> 1 : w >> 2;
-      const int col = 2 * m;
-      uint4* to = p.frag + ((static_cast<size_t>(c / 16) * p.tiles + col / 8) * 4 + q) * 32 + (col % 8) * 4 + ft;
+      const int column = 2 * m;
+      uint4* to = p.frag + ((static_cast<size_t>(c / 16) * p.tiles + column / 8) * 4 + q) * 32 + (column % 8) * 4 + ft;
       to[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       to[4] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) place(threadIdx.x + i * kPrepThreads, held[i]);
+    for (int c = threadIdx.x + kHeld * kPrepThreads; c < chunks; c += kPrepThreads) {
+      float v[8];
+      chunk(c, v);
+      place(c, v);
     }
     return;
   }
@@ -169,194 +201,377 @@ __global__ void __launch_bounds__(kThreads) w4a16_prepare_kernel(W4A16Params p) 
   const int job = blockIdx.x - p.M, split = job % p.t_splits, r0 = job / p.t_splits * 16;
   float acc[2][4] = {};
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  constexpr int kIter = kTWarpK / 32;
+  uint4 a[kIter], b[kIter], x[kIter][2];
 #pragma unroll
-  for (int i = 0; i < kTWarpK / 32; ++i) {
+  for (int i = 0; i < kIter; ++i) {
     const int k = split * kTSplit + warp * kTWarpK + i * 32 + t * 8;
-    uint4 a = zero, b = zero, x[2] = {zero, zero};
+    a[i] = b[i] = x[i][0] = x[i][1] = zero;
     if (k < p.K) {
-      a = __ldg(reinterpret_cast<const uint4*>(p.L1t + static_cast<size_t>(r0 + g) * p.K + k));
-      b = __ldg(reinterpret_cast<const uint4*>(p.L1t + static_cast<size_t>(r0 + g + 8) * p.K + k));
+      a[i] = __ldg(reinterpret_cast<const uint4*>(p.L1t + static_cast<size_t>(r0 + g) * p.K + k));
+      b[i] = __ldg(reinterpret_cast<const uint4*>(p.L1t + static_cast<size_t>(r0 + g + 8) * p.K + k));
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        if (j * 8 + g < p.M) x[j] = __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<size_t>(j * 8 + g) * p.K + k));
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (j * 8 >= p.M) break;
-      mma_bf16(acc[j], a.x, b.x, a.y, b.y, x[j].x, x[j].y);
-      mma_bf16(acc[j], a.z, b.z, a.w, b.w, x[j].z, x[j].w);
+        if (j * 8 + g < p.M)
+          x[i][j] = __ldg(reinterpret_cast<const uint4*>(p.X + static_cast<size_t>(j * 8 + g) * p.K + k));
     }
   }
+#pragma unroll
+  for (int i = 0; i < kIter; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      mma_bf16(acc[j], a[i].x, b[i].x, a[i].y, b[i].y, x[i][j].x, x[i][j].y);
+      mma_bf16(acc[j], a[i].z, b[i].z, a[i].w, b[i].w, x[i][j].z, x[i][j].w);
+    }
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) red[warp][g + 8 * (e >> 1)][j * 8 + 2 * t + (e & 1)] = acc[j][e];
   __syncthreads();
-  const int r = threadIdx.x % 16, m = threadIdx.x / 16;
+  const int r = threadIdx.x % 16, m = threadIdx.x / 16;  // m up to 31
   if (m < p.M) {
     float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += red[w][r][m];
+    for (int w = 0; w < kPrepWarps; ++w) s += red[w][r][m];
     p.T[(static_cast<size_t>(split) * p.M + m) * p.r_pad + r0 + r] = s;
   }
 }
 
-// One unit of 32 weight rows per CTA; its warps take the 128-wide steps of K in turn.
-template <bool INT4, int NT>
-__global__ void __launch_bounds__(kThreads) w4a16_kernel(W4A16Params p) {
-  __shared__ float red[kWarps][NT * 4][kUnitRows + 1];
-  __shared__ float s_t[kMaxTokens * 128];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t = lane & 3;
-  const int u = blockIdx.x;
-  const size_t row_bytes = p.K / 2;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
+// What a thread needs of the weights for one step: 32 weights of each of its 4 rows and their scales.  It
+// copies them to its own places of a ring in shared memory, [piece][lane] x 16 bytes per stage of a
+// warp, and reads only those back.
+struct Step {
+  uint4 w[4];
+  uint4 sc;
+};
+constexpr int kPieces = 5, kStageBytes = kPieces * 32 * 16, kStages = 3;
 
-  float acc[2][NT][4] = {};
-  for (int s = warp; s < p.steps; s += kWarps) {
-    uint4 w[4];
+// 16 or 8 bytes to shared memory, zeros if !in (`src` is then not read)
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(in ? 8 : 0) : "memory");
+}
+
+// Where a thread finds its part of a unit: its first row's codes and its scales, at step 0.
+struct Source {
+  const uint8_t* codes;
+  const uint8_t* sf;
+  int rows;  // of its 4 rows, those below N (the first ones)
+};
+template <bool INT4>
+__device__ __forceinline__ Source unit_source(const W4A16Params& p, int u, int g, int t) {
+  Source v;
+  const int n = unit_row<INT4>(u, 0, g);
+  v.rows = INT4 ? min(4, max(0, p.N - n)) : n < p.N ? min(4, (p.N - n + 31) / 32) : 0;
+  v.codes = p.codes + static_cast<size_t>(n < p.N ? n : 0) * (p.K / 2) + t * (INT4 ? 8 : 16);
+  if (INT4)  // of rows b = 0..3, bf16
+    v.sf = static_cast<const uint8_t*>(p.sf) + (u * kUnitRows + 4 * g) * 2;
+  else  // of rows b = 0..3 (a word each) and 64 columns
+    v.sf = static_cast<const uint8_t*>(p.sf) +
+           (static_cast<size_t>(u >> 2) * (p.K / 64) + (t >> 1)) * 512 + (8 * (u & 3) + g) * 16;
+  return v;
+}
+
+// Starts the copies of step s.
+template <bool INT4>
+__device__ __forceinline__ void fetch_step(const W4A16Params& p, const Source& from, int s, int t, uint32_t to) {
+  const uint8_t* row = from.codes + s * (kStep / 2);
+  const size_t next = static_cast<size_t>(INT4 ? 1 : 32) * (p.K / 2);
+  const bool second = s * kStep + 64 < p.K;  // the step's second 64 columns exist
+#pragma unroll
+  for (int b = 0; b < 4; ++b, to += 512) {
+    const bool in = b < from.rows;
+    const uint8_t* at = in ? row + b * next : p.codes;
+    if (INT4) {  // 8 bytes of each 64-wide group
+      copy8(to, at, in);
+      copy8(to + 8, second ? at + 32 : at, in && second);
+    } else {
+      const bool inside = in && (second || t < 2);
+      copy16(to, inside ? at : p.codes, inside);
+    }
+  }
+  if (INT4) {
+    const size_t group = static_cast<size_t>((p.N + 255) / 256) * 256 * 2;
+    const uint8_t* at = from.sf + 2 * s * group;
+    copy8(to, at, true);
+    copy8(to + 8, second ? at + group : at, second);
+  } else {
+    const bool inside = second || t < 2;
+    copy16(to, inside ? from.sf + static_cast<size_t>(s) * 1024 : static_cast<const uint8_t*>(p.sf), inside);
+  }
+}
+
+template <bool INT4, int NT>
+__device__ __forceinline__ void multiply_step(const W4A16Params& p, int s, int g, int t, int lane, const Step& v,
+                                              float (&acc)[2][NT][4]) {
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint4* frag = p.frag + static_cast<size_t>(s) * NT * 128 + lane;
+  uint4 x[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[j][q] = j * 8 + g < 2 * p.M ? frag[(j * 4 + q) * 32] : zero;
+  if (INT4) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const uint32_t c0 = half ? v.sc.z : v.sc.x, c1 = half ? v.sc.w : v.sc.y;
+      const float f[4] = {pair_lo(c0), pair_hi(c0), pair_lo(c1), pair_hi(c1)};
+      float sum[2][NT][4] = {};
+#pragma unroll
+      for (int q = 2 * half; q < 2 * half + 2; ++q) {
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile) {
+          uint32_t a[4], b[4];
+          int4_pairs((&v.w[2 * tile].x)[q], a);
+          int4_pairs((&v.w[2 * tile + 1].x)[q], b);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            mma_f16(sum[tile][j], a[0], b[0], a[1], b[1], x[j][q].x, x[j][q].y);
+            mma_f16(sum[tile][j], a[2], b[2], a[3], b[3], x[j][q].z, x[j][q].w);
+          }
+        }
+      }
+#pragma unroll
+      for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[tile][j][e] = __fmaf_rn(sum[tile][j][e], f[2 * tile + (e >> 1)], acc[tile][j][e]);
+    }
+  } else {
+    __half2 s01[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      uint32_t h;
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>((&v.sc.x)[b] >> (16 * (t & 1)))));
+      s01[b] = as_half2(h);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+#pragma unroll
+      for (int tile = 0; tile < 2; ++tile) {
+        uint32_t a[4], b[4];
+        e2m1_pairs((&v.w[2 * tile].x)[q], a);
+        e2m1_pairs((&v.w[2 * tile + 1].x)[q], b);
+        const __half2 sa = q < 2 ? __low2half2(s01[2 * tile]) : __high2half2(s01[2 * tile]);
+        const __half2 sb = q < 2 ? __low2half2(s01[2 * tile + 1]) : __high2half2(s01[2 * tile + 1]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          a[j] = as_u32(__hmul2(as_half2(a[j]), sa));
+          b[j] = as_u32(__hmul2(as_half2(b[j]), sb));
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma_f16(acc[tile][j], a[0], b[0], a[1], b[1], x[j][q].x, x[j][q].y);
+          mma_f16(acc[tile][j], a[2], b[2], a[3], b[3], x[j][q].z, x[j][q].w);
+        }
+      }
+    }
+  }
+}
+
+// The low-rank branch as MMA steps of 16 ranks: rows of L2 / alpha_w against the tokens' T over their
+// scale, as bf16 hi + lo columns.
+template <bool INT4, int NT>
+__device__ __forceinline__ void multiply_branch(const W4A16Params& p, const float* s_t, int u, int g, int t,
+                                                float (&acc)[2][NT][4]) {
+  for (int r = 0; r < p.r_pad; r += 16) {
+    uint2 l2[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       const int n = unit_row<INT4>(u, b, g);
-      const uint8_t* row = p.codes + n * row_bytes + s * (kStep / 2);
-      w[b] = zero;
-      if (n < p.N) {
-        if (INT4) {  // 8 bytes of each 64-wide group
-          const uint2 a = __ldg(reinterpret_cast<const uint2*>(row + t * 8));
-          w[b].x = a.x, w[b].y = a.y;
-          if (s * kStep + 64 < p.K) {
-            const uint2 c = __ldg(reinterpret_cast<const uint2*>(row + 32 + t * 8));
-            w[b].z = c.x, w[b].w = c.y;
-          }
-        } else if (s * kStep + t * 32 < p.K) {
-          w[b] = __ldg(reinterpret_cast<const uint4*>(row + t * 16));
-        }
+      l2[b] = n < p.N ? __ldg(reinterpret_cast<const uint2*>(p.L2t + static_cast<size_t>(n) * p.r_pad + r) + t)
+                      : make_uint2(0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int m = (j * 8 + g) >> 1;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (m < p.M) v = *reinterpret_cast<const float4*>(s_t + m * p.r_pad + r + 4 * t);
+      uint32_t b0 = bf16x2(v.x, v.y), b1 = bf16x2(v.z, v.w);
+      if (g & 1) {
+        b0 = bf16x2(rest(v.x, pair_lo(b0)), rest(v.y, pair_hi(b0)));
+        b1 = bf16x2(rest(v.z, pair_lo(b1)), rest(v.w, pair_hi(b1)));
+      }
+#pragma unroll
+      for (int tile = 0; tile < 2; ++tile)
+        mma_bf16(acc[tile][j], l2[2 * tile].x, l2[2 * tile + 1].x, l2[2 * tile].y, l2[2 * tile + 1].y, b0, b1);
+    }
+  }
+}
+
+// A CTA takes two units of 32 weight rows at a time; its warps, four per unit, and those of the other
+// CTAs of its cluster take the 128-wide steps of K in turn (p.groups in all).  Every warp leaves its
+// sums in shared memory, where each CTA of the cluster adds up a share of the outputs: the CTA's four
+// groups first, then the CTAs.  Copies of weights run two steps ahead of the products, over the ends of
+// units and ahead of the wait for the first kernel's results; what that kernel wrote is read through
+// L1, which the CTAs of an SM share.
+template <bool INT4, int NT>
+__global__ void __launch_bounds__(32 * kWarps, NT > 1 ? 2 : 3) w4a16_kernel(W4A16Params p) {
+  constexpr int kRows = kSlices * kUnitRows, kPitch = kRows + 8;  // a warp's stores fall into different banks
+  constexpr int kGroupFloats = NT * 4 * kPitch;
+  extern __shared__ __align__(16) uint8_t smem[];  // the warps' rings, then the groups' sums [kGroups][NT * 4 tokens][kPitch]
+  __shared__ __align__(16) float s_t[kMaxTokens * 128];  // T over the tokens' scales
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int slice = warp % kSlices, kg = warp / kSlices;
+  const int rank = blockIdx.x % p.cluster, block_step = gridDim.x / p.cluster;
+  const int first = rank * kGroups + kg;  // this warp's first step of a unit
+  const int jobs = p.M * kRows;
+  const uint32_t ring = smem_u32(smem) + warp * kStages * kStageBytes + lane * 16;
+  float* red = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes);
+
+  // this warp's steps, unit by unit, as they are fetched
+  int next_block = first < p.steps ? static_cast<int>(blockIdx.x) / p.cluster : p.blocks, next_step = first;
+  Source source = unit_source<INT4>(p, next_block * kSlices + slice, g, t);
+  auto fetch = [&](int stage) {
+    if (next_block < p.blocks) {
+      fetch_step<INT4>(p, source, next_step, t, ring + stage * kStageBytes);
+      next_step += p.groups;
+      if (next_step >= p.steps) {
+        next_step = first, next_block += block_step;
+        source = unit_source<INT4>(p, next_block * kSlices + slice, g, t);
       }
     }
-    uint4 x[NT][4];
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+  grid_dep_wait();
+  const bool branch = p.r_pad > 0 && rank == p.cluster - 1;  // has the last group of steps, which is the shortest
+  if (branch) {
+    for (int i = threadIdx.x; i < p.M * p.r_pad; i += blockDim.x) {
+      float v = 0.0f;
+      for (int k = 0; k < p.t_splits; k += 12) {  // all loads of K <= 12288 at once
+        float a[12];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        x[j][q] = j * 8 + g < 2 * p.M ? __ldg(p.frag + ((static_cast<size_t>(s) * NT + j) * 4 + q) * 32 + lane) : zero;
-
-    if (INT4) {
-      const uint16_t* sf = static_cast<const uint16_t*>(p.sf) + u * kUnitRows + 4 * g;
-      const size_t n_pad = static_cast<size_t>((p.N + 255) / 256) * 256;
+        for (int j = 0; j < 12; ++j)
+          a[j] = k + j < p.t_splits ? p.T[static_cast<size_t>(k + j) * p.M * p.r_pad + i] : 0.0f;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (s * kStep + half * 64 >= p.K) break;
-        const uint2 sc = __ldg(reinterpret_cast<const uint2*>(sf + (static_cast<size_t>(s) * 2 + half) * n_pad));
-        const float f[4] = {pair_lo(sc.x), pair_hi(sc.x), pair_lo(sc.y), pair_hi(sc.y)};
-#pragma unroll
-        for (int tile = 0; tile < 2; ++tile) {
-          float sum[NT][4] = {};
-#pragma unroll
-          for (int q = 2 * half; q < 2 * half + 2; ++q) {
-            uint32_t a[4], b[4];
-            int4_pairs((&w[2 * tile].x)[q], a);
-            int4_pairs((&w[2 * tile + 1].x)[q], b);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              mma_f16(sum[j], a[0], b[0], a[1], b[1], x[j][q].x, x[j][q].y);
-              mma_f16(sum[j], a[2], b[2], a[3], b[3], x[j][q].z, x[j][q].w);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[tile][j][e] = __fmaf_rn(sum[j][e], f[2 * tile + (e >> 1)], acc[tile][j][e]);
-        }
+        for (int j = 0; j < 12; ++j) v += a[j];
       }
+      s_t[i] = v * __frcp_rn(p.pow2[i / p.r_pad]);  // exact: a power of two
+    }
+    __syncthreads();
+  }
+
+  int stage = 0;
+  for (int block = blockIdx.x / p.cluster; block < p.blocks; block += block_step) {
+    const int unit0 = block * kSlices, u = unit0 + slice;
+    float acc[2][NT][4] = {};
+    if (branch && kg == kGroups - 1) multiply_branch<INT4, NT>(p, s_t, u, g, t, acc);
+    for (int s = first; s < p.steps; s += p.groups) {
+      fetch(stage ? stage - 1 : kStages - 1);  // the stage read last
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      Step v;
+      const uint32_t from = ring + stage * kStageBytes;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) v.w[b] = lds128(from + b * 512);
+      v.sc = lds128(from + 4 * 512);
+      multiply_step<INT4, NT>(p, s, g, t, lane, v, acc);
+      if (++stage == kStages) stage = 0;
+    }
+
+    // a thread holds a token's hi and lo columns side by side: their sum
+#pragma unroll
+    for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          red[kg * kGroupFloats + (j * 4 + t) * kPitch + slice * kUnitRows + (2 * tile + h) * 8 + g] =
+              acc[tile][j][2 * h] + acc[tile][j][2 * h + 1];
+    __syncthreads();
+    auto four = [&](int at) {
+      const float* r = red + at;
+      return ((r[0] + r[kGroupFloats]) + r[2 * kGroupFloats]) + r[3 * kGroupFloats];
+    };
+    auto finish = [&](int i, float v) {
+      const int m = i / kRows, row = i % kRows, n = unit_row<INT4>(unit0 + row / kUnitRows, (row >> 3) & 3, row & 7);
+      if (n >= p.N) return;
+      const __nv_bfloat16 y = __float2bfloat16_rn(__fmaf_rn(v, p.pow2[m] * p.alpha_w, __ldg(p.bias + n)));
+      p.Y[static_cast<size_t>(m) * p.N + n] = *reinterpret_cast<const uint16_t*>(&y);
+    };
+    if (p.cluster == 1) {
+      for (int i = threadIdx.x; i < jobs; i += blockDim.x) finish(i, four(i / kRows * kPitch + i % kRows));
+      __syncthreads();  // before the next units' sums
     } else {
-      // scales of rows b = 0..3 and columns 64 kb..64 kb + 63; this thread's 32 weights are two groups
-      const int kb = 2 * s + (t >> 1);
-      uint4 sc = zero;
-      if (kb < p.K / 64)
-        sc = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.sf) +
-                                                  (static_cast<size_t>(u >> 2) * (p.K / 64) + kb) * 512) +
-                   8 * (u & 3) + g);
-      __half2 s01[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>((&sc.x)[b] >> (16 * (t & 1)))));
-        s01[b] = as_half2(h);
+      for (int i = threadIdx.x; i < jobs; i += blockDim.x) {
+        const int at = i / kRows * kPitch + i % kRows;
+        red[at] = four(at);
       }
+      cluster_sync_all();
+      const uint32_t mine = smem_u32(red);
+      const int share = jobs / p.cluster;  // neighbouring outputs to neighbouring lanes: rows of 128 bytes
+      for (int i = rank * share + threadIdx.x; i < (rank + 1) * share; i += blockDim.x) {
+        const int at = i / kRows * kPitch + i % kRows;
+        float fours[8];
 #pragma unroll
-      for (int tile = 0; tile < 2; ++tile) {
+        for (int c = 0; c < 8; ++c) fours[c] = c < p.cluster ? ld_dsmem_f32(mapa_shared(mine, c) + at * 4) : 0.0f;
+        float v = fours[0];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t a[4], b[4];
-          e2m1_pairs((&w[2 * tile].x)[q], a);
-          e2m1_pairs((&w[2 * tile + 1].x)[q], b);
-          const __half2 sa = q < 2 ? __low2half2(s01[2 * tile]) : __high2half2(s01[2 * tile]);
-          const __half2 sb = q < 2 ? __low2half2(s01[2 * tile + 1]) : __high2half2(s01[2 * tile + 1]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            a[j] = as_u32(__hmul2(as_half2(a[j]), sa));
-            b[j] = as_u32(__hmul2(as_half2(b[j]), sb));
-          }
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            mma_f16(acc[tile][j], a[0], b[0], a[1], b[1], x[j][q].x, x[j][q].y);
-            mma_f16(acc[tile][j], a[2], b[2], a[3], b[3], x[j][q].z, x[j][q].w);
-          }
-        }
+        for (int c = 1; c < 8; ++c) v += fours[c];
+        finish(i, v);
       }
+      cluster_sync_all();  // the others may still read this CTA's sums
     }
-  }
-
-  // a thread holds a token's hi and lo columns side by side: their sum, then the sum over the warps
-#pragma unroll
-  for (int tile = 0; tile < 2; ++tile)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        red[warp][j * 4 + t][(2 * tile + h) * 8 + g] = acc[tile][j][2 * h] + acc[tile][j][2 * h + 1];
-  for (int i = threadIdx.x; i < p.M * p.r_pad; i += kThreads) {
-    float v = 0.0f;
-    for (int j = 0; j < p.t_splits; ++j) v += p.T[static_cast<size_t>(j) * p.M * p.r_pad + i];
-    s_t[i] = v * p.alpha_w;  // exact, and keeps the products with L2 / alpha_w in range
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.M * kUnitRows; i += kThreads) {
-    const int m = i / kUnitRows, row = i % kUnitRows;
-    const int n = unit_row<INT4>(u, row >> 3, row & 7);
-    if (n >= p.N) continue;
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += red[w][m][row];
-    v *= p.pow2[m] * p.alpha_w;
-    const uint4* l2 = reinterpret_cast<const uint4*>(p.L2t + static_cast<size_t>(n) * p.r_pad);
-    float low = 0.0f;
-    for (int r = 0; r < p.r_pad / 8; ++r) {
-      float f[8];
-      unpack8(__ldg(l2 + r), f, static_cast<const __nv_bfloat16*>(nullptr));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) low = __fmaf_rn(s_t[m * p.r_pad + r * 8 + j], f[j], low);
-    }
-    const __nv_bfloat16 y = __float2bfloat16_rn(v + low + p.bias[n]);
-    p.Y[static_cast<size_t>(m) * p.N + n] = *reinterpret_cast<const uint16_t*>(&y);
   }
 }
 
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 int column_tiles(int M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
 
-template <bool INT4>
-svdq_status launch(const W4A16Params& p, cudaStream_t stream) {
-  w4a16_prepare_kernel<INT4><<<p.M + p.r_pad / 16 * p.t_splits, kThreads, 0, stream>>>(p);
-  SVDQ_CUDA_TRY(cudaGetLastError());
+// How the steps of K are shared out: to the 4 groups of one CTA, or to 8, 16 or 32 (a cluster of CTAs)
+// while there are steps for them and the device still has fewer than two thousand warps.  The number
+// depends on the layer alone, so a token's sums are the same for any M.
+int step_groups(int N, int steps) {
+  const int units = (N + kUnitRows - 1) / kUnitRows;
+  int groups = kGroups;
+  while (groups < 8 * kGroups && groups < steps && units * groups < 2048) groups *= 2;
+  return groups;
+}
+
+template <bool INT4, int NT>
+svdq_status launch_main(W4A16Params& p, cudaStream_t stream) {
+  p.cluster = p.groups / kGroups;
   const int units = INT4 ? (p.N + kUnitRows - 1) / kUnitRows : (p.N + 127) / 128 * 4;
-  switch (p.tiles) {
-    case 1: w4a16_kernel<INT4, 1><<<units, kThreads, 0, stream>>>(p); break;
-    case 2: w4a16_kernel<INT4, 2><<<units, kThreads, 0, stream>>>(p); break;
-    default: w4a16_kernel<INT4, 4><<<units, kThreads, 0, stream>>>(p); break;
-  }
-  SVDQ_CUDA_TRY(cudaGetLastError());
+  p.blocks = (units + kSlices - 1) / kSlices;
+  const size_t smem = static_cast<size_t>(kWarps) * kStages * kStageBytes +
+                      static_cast<size_t>(kGroups) * NT * 4 * (kSlices * kUnitRows + 8) * sizeof(float);
+  // as many CTAs as the SMs hold at a time, so that the units are dealt out evenly
+  const int resident = kSMs * (NT > 1 ? 2 : 3);
+  const int grid = p.cluster > 1 || p.blocks < resident ? p.blocks : resident;
+  SVDQ_CUDA_TRY(cudaFuncSetAttribute(w4a16_kernel<INT4, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(smem)));
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid * p.cluster);
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+  SVDQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, w4a16_kernel<INT4, NT>, p));
   return SVDQ_OK;
+}
+
+template <bool INT4>
+svdq_status launch(W4A16Params& p, cudaStream_t stream) {
+  w4a16_prepare_kernel<INT4><<<p.M + p.r_pad / 16 * p.t_splits, kPrepThreads, 0, stream>>>(p);
+  SVDQ_CUDA_TRY(cudaGetLastError());
+  switch (p.tiles) {
+    case 1: return launch_main<INT4, 1>(p, stream);
+    case 2: return launch_main<INT4, 2>(p, stream);
+    default: return launch_main<INT4, 4>(p, stream);
+  }
 }
 
 }  // namespace
@@ -384,6 +599,7 @@ svdq_status launch_w4a16(const svdq_weights* w, const void* X, int M, void* Y, v
   p.steps = (w->K + kStep - 1) / kStep;
   p.tiles = column_tiles(M);
   p.t_splits = (w->K + kTSplit - 1) / kTSplit;
+  p.groups = step_groups(w->N, p.steps);
   p.alpha_w = w->alpha_w;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.frag = reinterpret_cast<uint4*>(ws);
