@@ -308,66 +308,56 @@ __device__ __forceinline__ void multiply_step(const W4A16Params& p, int s, int g
                                               float (&acc)[2][NT][4]) {
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const uint4* frag = p.frag + static_cast<size_t>(s) * NT * 128 + lane;
-  uint4 x[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) x[j][q] = j * 8 + g < 2 * p.M ? frag[(j * 4 + q) * 32] : zero;
-  if (INT4) {
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const uint32_t c0 = half ? v.sc.z : v.sc.x, c1 = half ? v.sc.w : v.sc.y;
-      const float f[4] = {pair_lo(c0), pair_hi(c0), pair_lo(c1), pair_hi(c1)};
-      float sum[2][NT][4] = {};
-#pragma unroll
-      for (int q = 2 * half; q < 2 * half + 2; ++q) {
-#pragma unroll
-        for (int tile = 0; tile < 2; ++tile) {
-          uint32_t a[4], b[4];
-          int4_pairs((&v.w[2 * tile].x)[q], a);
-          int4_pairs((&v.w[2 * tile + 1].x)[q], b);
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            mma_f16(sum[tile][j], a[0], b[0], a[1], b[1], x[j][q].x, x[j][q].y);
-            mma_f16(sum[tile][j], a[2], b[2], a[3], b[3], x[j][q].z, x[j][q].w);
-          }
-        }
-      }
-#pragma unroll
-      for (int tile = 0; tile < 2; ++tile)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[tile][j][e] = __fmaf_rn(sum[tile][j][e], f[2 * tile + (e >> 1)], acc[tile][j][e]);
-    }
-  } else {
-    __half2 s01[4];
+  __half2 s01[4];  // NVFP4: the scales of this thread's two groups, per row
+  if (!INT4) {
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       uint32_t h;
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>((&v.sc.x)[b] >> (16 * (t & 1)))));
       s01[b] = as_half2(h);
     }
+  }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+  for (int half = 0; half < 2; ++half) {
+    uint4 x[NT][2];
 #pragma unroll
-      for (int tile = 0; tile < 2; ++tile) {
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) x[j][q] = j * 8 + g < 2 * p.M ? frag[(j * 4 + 2 * half + q) * 32] : zero;
+#pragma unroll
+    for (int tile = 0; tile < 2; ++tile) {
+      float sum[NT][4] = {};  // INT4: of one group
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
         uint32_t a[4], b[4];
-        e2m1_pairs((&v.w[2 * tile].x)[q], a);
-        e2m1_pairs((&v.w[2 * tile + 1].x)[q], b);
-        const __half2 sa = q < 2 ? __low2half2(s01[2 * tile]) : __high2half2(s01[2 * tile]);
-        const __half2 sb = q < 2 ? __low2half2(s01[2 * tile + 1]) : __high2half2(s01[2 * tile + 1]);
+        if (INT4) {
+          int4_pairs((&v.w[2 * tile].x)[2 * half + q], a);
+          int4_pairs((&v.w[2 * tile + 1].x)[2 * half + q], b);
+        } else {
+          e2m1_pairs((&v.w[2 * tile].x)[2 * half + q], a);
+          e2m1_pairs((&v.w[2 * tile + 1].x)[2 * half + q], b);
+          const __half2 sa = half ? __high2half2(s01[2 * tile]) : __low2half2(s01[2 * tile]);
+          const __half2 sb = half ? __high2half2(s01[2 * tile + 1]) : __low2half2(s01[2 * tile + 1]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          a[j] = as_u32(__hmul2(as_half2(a[j]), sa));
-          b[j] = as_u32(__hmul2(as_half2(b[j]), sb));
+          for (int j = 0; j < 4; ++j) {
+            a[j] = as_u32(__hmul2(as_half2(a[j]), sa));
+            b[j] = as_u32(__hmul2(as_half2(b[j]), sb));
+          }
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          mma_f16(acc[tile][j], a[0], b[0], a[1], b[1], x[j][q].x, x[j][q].y);
-          mma_f16(acc[tile][j], a[2], b[2], a[3], b[3], x[j][q].z, x[j][q].w);
+          float(&to)[4] = INT4 ? sum[j] : acc[tile][j];
+          mma_f16(to, a[0], b[0], a[1], b[1], x[j][q].x, x[j][q].y);
+          mma_f16(to, a[2], b[2], a[3], b[3], x[j][q].z, x[j][q].w);
         }
+      }
+      if (INT4) {
+        const uint32_t c = tile ? (half ? v.sc.w : v.sc.y) : (half ? v.sc.z : v.sc.x);  // rows 2 tile, 2 tile + 1
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[tile][j][e] = __fmaf_rn(sum[j][e], e < 2 ? pair_lo(c) : pair_hi(c), acc[tile][j][e]);
       }
     }
   }
@@ -410,11 +400,11 @@ __device__ __forceinline__ void multiply_branch(const W4A16Params& p, const floa
 // units and ahead of the wait for the first kernel's results; what that kernel wrote is read through
 // L1, which the CTAs of an SM share.
 template <bool INT4, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT > 1 ? 2 : 3) w4a16_kernel(W4A16Params p) {
+__global__ void __launch_bounds__(32 * kWarps, NT > 2 ? 2 : 3) w4a16_kernel(W4A16Params p) {
   constexpr int kRows = kSlices * kUnitRows, kPitch = kRows + 8;  // a warp's stores fall into different banks
   constexpr int kGroupFloats = NT * 4 * kPitch;
-  extern __shared__ __align__(16) uint8_t smem[];  // the warps' rings, then the groups' sums [kGroups][NT * 4 tokens][kPitch]
-  __shared__ __align__(16) float s_t[kMaxTokens * 128];  // T over the tokens' scales
+  extern __shared__ __align__(16) uint8_t smem[];  // the warps' rings, the groups' sums
+                                                   // [kGroups][NT * 4 tokens][kPitch], T over the tokens' scales
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int slice = warp % kSlices, kg = warp / kSlices;
@@ -423,6 +413,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT > 1 ? 2 : 3) w4a16_kernel(W4A1
   const int jobs = p.M * kRows;
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStageBytes + lane * 16;
   float* red = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes);
+  float* s_t = red + kGroups * kGroupFloats;
 
   // this warp's steps, unit by unit, as they are fetched
   int next_block = first < p.steps ? static_cast<int>(blockIdx.x) / p.cluster : p.blocks, next_step = first;
@@ -540,9 +531,10 @@ svdq_status launch_main(W4A16Params& p, cudaStream_t stream) {
   const int units = INT4 ? (p.N + kUnitRows - 1) / kUnitRows : (p.N + 127) / 128 * 4;
   p.blocks = (units + kSlices - 1) / kSlices;
   const size_t smem = static_cast<size_t>(kWarps) * kStages * kStageBytes +
-                      static_cast<size_t>(kGroups) * NT * 4 * (kSlices * kUnitRows + 8) * sizeof(float);
+                      static_cast<size_t>(kGroups) * NT * 4 * (kSlices * kUnitRows + 8) * sizeof(float) +
+                      static_cast<size_t>(p.M) * p.r_pad * sizeof(float);
   // as many CTAs as the SMs hold at a time, so that the units are dealt out evenly
-  const int resident = kSMs * (NT > 1 ? 2 : 3);
+  const int resident = kSMs * (NT > 2 ? 2 : 3);
   const int grid = p.cluster > 1 || p.blocks < resident ? p.blocks : resident;
   SVDQ_CUDA_TRY(cudaFuncSetAttribute(w4a16_kernel<INT4, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      static_cast<int>(smem)));
