@@ -4,15 +4,23 @@
 // With y += (x A) B: dA = X^T (dY B^T) and dB^T = dY^T (X A), both this product.  X is the large
 // operand (M K values against (M + K) r), so the kernel is bound by reading it once as long as the
 // 2 M K r operations keep up; they run on the tensor cores (mma.sync m16n8k16, bf16 inputs, fp32
-// sums).  X needs no copy or transpose: the contraction runs over rows, so each thread reads the
-// same 8 consecutive columns of 4 rows and pairs the rows' values in registers.  Checkpoint values
-// are q 2^e with at most 7 significant bits, exact in bf16.
+// sums), the columns of X as the M side.  The contraction runs over rows, so a thread takes the same
+// columns of 4 rows and pairs the rows' values in registers: X is never transposed or stored again.
 //
-// The tensor cores' additions truncate, which would add up over thousands of tokens, so a warp sums
-// at most some 300 tokens in one accumulator; those sums are joined by ordinary fp32 additions, in
-// a fixed order: over the CTA's warps in shared memory, over the CTAs by a second kernel.
+// A checkpoint's codes are exact in bf16 as they are.  Their scales, powers of two, multiply the
+// fragments of S (exact), which costs 2 products per 16 rows and 8 columns of S instead of one per
+// value of X; a warp's 64 columns are two scale groups and each MMA stays in one.
+//
+// A CTA holds its rows of S in shared memory; each warp copies its 16 x 64 tiles of X ahead through a
+// ring of its own, so the main loop has no CTA barrier.  Sums are joined by ordinary fp32 additions in
+// a fixed order: the CTA's row warps in shared memory, then the CTAs that share the rows by a second kernel
+// over partial results.  (Clusters in its place left SMs idle: at one CTA of 16 warps per SM 45 clusters of 3
+// or 15 of 8 are resident, not 49 or 18.)
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
+#include "ptx.cuh"
 #include "rows.cuh"
 #include "svdq_internal.h"
 
@@ -22,18 +30,19 @@ namespace {
 using namespace dev;
 
 constexpr int kSMs = 148;
-constexpr int kWarpCols = 64;                  // columns of X per warp: 8 lanes x 8
-constexpr int kColWarps = 2, kRowWarps = 4;    // warps along the columns and along the rows
-constexpr int kCtaCols = kWarpCols * kColWarps;
-constexpr int kCtaRows = 16 * kRowWarps;       // rows per step of the CTA
-constexpr int kThreads = 32 * kColWarps * kRowWarps;
+constexpr int kTileCols = 64;          // of X per warp step, 16 rows (bf16) or 32
+constexpr int kWarps = 16, kThreads = 32 * kWarps;
+constexpr int kSBytes = 96 * 1024;    // of S in shared memory at a time
+constexpr int kMaxRows = 512;         // of one warp between two joins
 
 struct WgradParams {
-  const void* X;  // bf16 [M, K], or the codes
+  const uint8_t* X;       // bf16 [M, K], or the codes
   const uint8_t* scales;
-  const uint16_t* S;  // bf16 [M, r]
-  float* out;         // G, or the partial sums [splits][K][r]
-  int M, K, r, steps; // steps: row steps of kCtaRows per split
+  const uint16_t* S;      // bf16 [M, r]
+  float* out;             // G, or the partial sums [parts][K][r]
+  int M, K, r;
+  int col_warps;          // 1, 2 or 4; the others of the 16 warps share out the rows
+  int rows;               // per CTA, a multiple of a step's rows
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -44,64 +53,97 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
+// 16 bytes to shared memory, zeros if !in
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t scale_pair(uint32_t values, uint32_t pow2) {
+  const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&values),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&pow2));
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Pairs over two rows of 8 columns: w[j] holds (row a, row b) of column j.
+// A stage of a warp's ring: 16-byte pieces of 64 values of each row, placed so that the four rows a warp
+// reads at a time fall into different banks, then 8 bytes per row around its two scale bytes.  A step
+// of codes takes 32 rows, which halves what the copies and the scales cost a value.
 template <int SRC>
-__device__ __forceinline__ void pair_rows(const uint4& a, const uint4& b, float sa, float sb, uint32_t (&w)[8]) {
+struct Tile {
+  static constexpr int rows = SRC ? 32 : 16, stages = SRC ? 3 : 4;
+  static constexpr int piece_values = SRC ? 16 : 8;
+  static constexpr int pieces = kTileCols / piece_values;  // per row
+  static constexpr int scales = rows * pieces * 16;
+  static constexpr int bytes = scales + (SRC ? rows * 8 : 0);
+  __device__ static uint32_t at(int row, int piece) {
+    return SRC ? (row >> 1) * 128 + ((((row & 1) << 2 | piece) ^ (((row >> 1) & 3) << 1)) << 4)
+               : row * 128 + ((piece ^ (((row >> 1) & 1) << 2)) << 4);
+  }
+};
+
+// Where piece `j` (8 columns) of row `row` of S lies: NT pieces a row, spread over the banks.
+template <int NT>
+__device__ __forceinline__ uint32_t s_place(int row, int j) {
+  return (row * NT + (j ^ ((row / (8 / NT)) & (NT - 1)))) * 16;
+}
+
+// Pairs over two rows of four columns of a tile: the words at `a` (one row) and `b` (the next).
+template <int SRC>
+__device__ __forceinline__ void pair_rows(uint32_t at_a, uint32_t at_b, uint32_t (&w)[4]) {
   if (SRC == 0) {
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    const uint2 a = lds64(at_a), b = lds64(at_b);
+    w[0] = __byte_perm(a.x, b.x, 0x5410), w[1] = __byte_perm(a.x, b.x, 0x7632);
+    w[2] = __byte_perm(a.y, b.y, 0x5410), w[3] = __byte_perm(a.y, b.y, 0x7632);
+  } else if (SRC == 1) {
+    // u = q + 128 = 128 h + u7; bf16 has 7 mantissa bits: (128 + u7) - (256 - 128 h), exact, both rows at once
+    const uint32_t a = lds32(at_a) ^ 0x80808080u, b = lds32(at_b) ^ 0x80808080u;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      w[2 * j] = __byte_perm(x[j], y[j], 0x5410);
-      w[2 * j + 1] = __byte_perm(x[j], y[j], 0x7632);
+      const uint32_t v = __byte_perm(a, b, 0x4400 + 0x1111 * j);  // bytes j of a, -, j of b, -
+      const uint32_t u = (v & 0x007F007Fu) | 0x43004300u, c = (v & 0x00800080u) ^ 0x43804380u;
+      const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&c));
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
     }
   } else {
-    constexpr int F = SRC == 1 ? SVDQ_CKPT8_INT8 : SVDQ_CKPT8_E4M3;
-    float u[8], v[8];
-    ckpt_values4<F>(a.x, sa, u);
-    ckpt_values4<F>(a.y, sa, u + 4);
-    ckpt_values4<F>(b.x, sb, v);
-    ckpt_values4<F>(b.y, sb, v + 4);
+    float x[4], y[4];
+    ckpt_values4<SVDQ_CKPT8_E4M3>(lds32(at_a), 1.0f, x);
+    ckpt_values4<SVDQ_CKPT8_E4M3>(lds32(at_b), 1.0f, y);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = bf16_pair(u[j], v[j]);
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[j], y[j]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
   }
 }
 
-// The raw 8 columns at (m, k) and their scale; zeros outside.
-template <int SRC>
-__device__ __forceinline__ void fetch(const WgradParams& p, int m, int k, uint4& v, uint32_t& scale) {
-  v = make_uint4(0, 0, 0, 0);
-  scale = 0;
-  if (m >= p.M || k >= p.K) return;
-  const size_t at = static_cast<size_t>(m) * p.K + k;
-  if (SRC == 0) {
-    v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.X) + at));
-  } else {
-    const uint2 c = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.X) + at));
-    v.x = c.x, v.y = c.y;
-    scale = __ldg(p.scales + static_cast<size_t>(m) * ((p.K + kCkptGroup - 1) / kCkptGroup) + k / kCkptGroup);
-  }
-}
-
-// NT: columns of S per CTA in tiles of 8.  blockIdx: x columns of X, y row split, z columns of S.
+// NT: columns of S per CTA in tiles of 8.  blockIdx: x columns of X, y CTA of the rows, z columns of S.
 template <int SRC, int NT>
 __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
-  constexpr int kLd = NT * 8 + 8;  // bf16 per row of the S tile: rows fall into different banks
-  // the S tiles of the loop, then the sums that the row warps join
-  constexpr int kTileBytes = 2 * kCtaRows * kLd * 2, kSumBytes = kCtaCols * (NT * 8 + 1) * 4;
-  __shared__ __align__(16) uint8_t smem[kTileBytes > kSumBytes ? kTileBytes : kSumBytes];
-  auto* s_tile = reinterpret_cast<uint16_t(*)[kCtaRows][kLd]>(smem);
-  auto* s_sum = reinterpret_cast<float(*)[NT * 8 + 1]>(smem);
+  extern __shared__ __align__(128) uint8_t smem[];  // S, then the rings; at the end the warps' sums
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int cw = warp % kColWarps, rw = warp / kColWarps;
-  const int k = blockIdx.x * kCtaCols + cw * kWarpCols + g * 8;
+  const int cw = warp % p.col_warps, rw = warp / p.col_warps, row_warps = kWarps / p.col_warps;
+  const int k0 = (blockIdx.x * p.col_warps + cw) * kTileCols;
   const int n0 = blockIdx.z * NT * 8;
-  const int row0 = blockIdx.y * p.steps * kCtaRows;
+  const int row0 = blockIdx.y * p.rows, row_end = min(p.M, row0 + p.rows);
+  const int groups = (p.K + kCkptGroup - 1) / kCkptGroup;
+  const uint32_t s_tile = smem_u32(smem);
+  const uint32_t ring = s_tile + kSBytes + warp * Tile<SRC>::stages * Tile<SRC>::bytes;
+  const int block_rows = row_warps * Tile<SRC>::rows;                      // of one step of the CTA
+  const int s_steps = kSBytes / (NT * 16) / block_rows;              // steps whose rows of S fit
 
   float acc[4][NT][4];
 #pragma unroll
@@ -109,129 +151,268 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.0f;
 
-  uint4 x[4];
-  uint32_t sc[4];
-  auto fetch_rows = [&](int step) {
-    const int m = row0 + step * kCtaRows + rw * 16 + 2 * t;
+  // this lane's part of the warp's next tile: 16-byte pieces of rows `fetch_row`, + 8 or + 4, ...
+  using Tl = Tile<SRC>;
+  constexpr int kTileRows = Tl::rows, kStages = Tl::stages;
+  constexpr int kRowsAtOnce = 32 / Tl::pieces;
+  const int piece = lane % Tl::pieces, piece_k = k0 + piece * Tl::piece_values, fetch_row = lane / Tl::pieces;
+  const size_t row_bytes = static_cast<size_t>(p.K) * (SRC ? 1 : 2);
+  const uint8_t* next_x = p.X + (row0 + rw * kTileRows + fetch_row) * row_bytes + static_cast<size_t>(piece_k) * (SRC ? 1 : 2);
+  const uint8_t* next_s = SRC ? p.scales + static_cast<size_t>(row0 + rw * kTileRows + lane) * groups + k0 / kCkptGroup
+                              : nullptr;
+  const uint8_t* scales_end = SRC ? p.scales + static_cast<size_t>(p.M) * groups : nullptr;
+  int fetch_left = piece_k < p.K ? row_end - row0 - rw * kTileRows : 0;  // rows from the tile's first to the end
+  int scale_left = k0 < p.K ? row_end - row0 - rw * kTileRows - lane : 0;
+  auto fetch = [&](int stage) {
+    const uint32_t to = ring + stage * Tl::bytes;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) fetch<SRC>(p, step < p.steps ? m + (i & 1) + (i >> 1) * 8 : p.M, k, x[i], sc[i]);
-  };
-  auto stage_s = [&](int step, int buf) {
-    const int m0 = row0 + step * kCtaRows;
-    for (int i = threadIdx.x; i < kCtaRows * NT * 8; i += kThreads) {
-      const int m = m0 + i / (NT * 8), n = n0 + i % (NT * 8);
-      s_tile[buf][i / (NT * 8)][i % (NT * 8)] = m < p.M && n < p.r ? p.S[static_cast<size_t>(m) * p.r + n] : 0;
+    for (int i = 0; i < kTileRows / kRowsAtOnce; ++i) {
+      const int row = i * kRowsAtOnce + fetch_row;
+      const bool in = row < fetch_left;
+      copy16(to + Tl::at(row, piece), in ? next_x + i * kRowsAtOnce * row_bytes : p.X, in);
     }
+    if (SRC && scale_left > 0) {  // the aligned words around a row's scale bytes
+      const uint32_t skip = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(next_s)) & 3;
+      const uint8_t* word = next_s - skip;
+      const uint32_t at = to + Tl::scales + lane * 8 - s_tile;
+      if (word >= p.scales && word + (skip == 3 ? 8 : 4) <= scales_end) {
+        copy4_async(smem + at, word);
+        if (skip == 3) copy4_async(smem + at + 4, word + 4);
+      } else {  // the array's first or last bytes
+        for (int b = 0; b < 8; ++b)
+          if (word + b >= p.scales && word + b < scales_end) smem[at + b] = word[b];
+      }
+    }
+    next_x += block_rows * row_bytes;
+    fetch_left -= block_rows;
+    if (SRC) next_s += static_cast<size_t>(block_rows) * groups, scale_left -= block_rows;
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  // where this lane finds rows 2 t (and, by other bits of the address, 2 t + 1, + 8, the second 32 columns)
+  const uint32_t x_at = SRC ? t * 128 + (((g >> 2) ^ (t << 1)) << 4) + (g & 3) * 4
+                            : t * 256 + (((g >> 1) ^ ((t & 1) << 2)) << 4) + (g & 1) * 8;
+  // the scale bytes of row `lane` of a tile
+  const uint32_t my_byte0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.scales)) + k0 / kCkptGroup;
+  const bool second = k0 + 32 < p.K;  // the columns' second group exists
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
-  fetch_rows(0);
-  stage_s(0, 0);
-  __syncthreads();
-  for (int step = 0; step < p.steps; ++step) {
-    uint32_t lo[8], hi[8];  // rows 2t, 2t+1 and 2t+8, 2t+9
-    pair_rows<SRC>(x[0], x[1], ckpt_scale(sc[0]), ckpt_scale(sc[1]), lo);
-    pair_rows<SRC>(x[2], x[3], ckpt_scale(sc[2]), ckpt_scale(sc[3]), hi);
-    fetch_rows(step + 1);
-    uint32_t b[NT][2];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const uint32_t at = static_cast<uint32_t>(
-          __cvta_generic_to_shared(&s_tile[step & 1][rw * 16 + (lane & 15)][j * 8]));
-      asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
-                   : "=r"(b[j][0]), "=r"(b[j][1])
-                   : "r"(at));
+  int stage = 0;
+  for (int row = row0; row < row_end; row += s_steps * block_rows) {
+    const int n_rows = min(s_steps * block_rows, row_end - row);
+    const int n_steps = (n_rows + block_rows - 1) / block_rows;
+    __syncthreads();  // the rows of S before these are done with
+    const bool wide = p.r % 8 == 0;
+    for (int i = threadIdx.x; i < n_steps * block_rows * NT; i += kThreads) {
+      const int m = i / NT, j = i % NT, n = n0 + j * 8;
+      const bool in = m < n_rows && n < p.r;
+      const uint16_t* from = p.S + static_cast<size_t>(row + m) * p.r + n;
+      const uint32_t to = s_tile + s_place<NT>(m, j);
+      if (wide) {
+        copy16(to, in ? from : p.S, in);
+      } else {
+        uint16_t* v = reinterpret_cast<uint16_t*>(smem + (to - s_tile));
+        for (int e = 0; e < 8; ++e) v[e] = in && n + e < p.r ? from[e] : 0;
+      }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t a[4] = {lo[2 * i], lo[2 * i + 1], hi[2 * i], hi[2 * i + 1]};
-#pragma unroll
-      for (int j = 0; j < NT; ++j) mma_bf16(acc[i][j], a, b[j][0], b[j][1]);
-    }
-    if (step + 1 < p.steps) stage_s(step + 1, (step + 1) & 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
-  }
 
-  // the row warps add their sums in turn
-  for (int w = 0; w < kRowWarps; ++w) {
-    if (rw == w) {
+    for (int step = 0; step < n_steps; ++step) {
+      fetch(stage ? stage - 1 : kStages - 1);  // the stage read last
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();
+      const uint32_t tile = ring + stage * Tile<SRC>::bytes;
+      const int local = step * block_rows + rw * kTileRows, m0 = row + local;
+      if (++stage == kStages) stage = 0;
+      if (m0 >= row_end) continue;  // the warp's last tiles; k0 >= K reads what no one reads back
+
+      // 2^(byte - 127) as bf16 of rows (lane, lane + 1), for both groups; rows beyond M: 0
+      uint32_t pow2[2] = {0, 0};
+      if (SRC) {
+        const int m = m0 + lane;
+        const uint32_t at = tile + Tl::scales + lane * 8 +
+                            ((my_byte0 + static_cast<uint32_t>(m) * static_cast<uint32_t>(groups)) & 3);
+        const uint32_t first = lds8(at), other = lds8(at + 1);
+        uint32_t both = (first ? first << 7 : 0x40u) | (other ? other << 7 : 0x40u) << 16;
+        if (!second) both &= 0xFFFFu;
+        if (m >= row_end) both = 0;
+        const uint32_t next = __shfl_down_sync(0xffffffffu, both, 1);
+        pow2[0] = __byte_perm(both, next, 0x5410);
+        pow2[1] = __byte_perm(both, next, 0x7632);
+      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int sub = 0; sub < kTileRows / 16; ++sub) {
+        uint32_t b[NT][2];
+        const uint32_t s_at = s_tile + (local + 16 * sub) * NT * 16 + s_place<NT>(lane & 15, NT == 1 ? 0 : lane >> 4);
+        if (NT == 1) {
+          asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
+                       : "=r"(b[0][0]), "=r"(b[0][1])
+                       : "r"(s_at));
+        } else {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+          for (int j = 0; j + 1 < NT; j += 2)
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(b[j][0]), "=r"(b[j][1]), "=r"(b[j + 1][0]), "=r"(b[j + 1][1])
+                         : "r"(s_at ^ (j * 16)));
+        }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float* s = &s_sum[cw * kWarpCols + g * 8 + 2 * i + (e >> 1)][j * 8 + 2 * t + (e & 1)];
-            *s = w ? *s + acc[i][j][e] : acc[i][j][e];
+        for (int half = 0; half < 2; ++half) {  // the two scale groups: columns 32 half + 4 g..4 g + 3
+          uint32_t lo[4], hi[4];
+          const uint32_t at = (tile + x_at) ^ (SRC ? 32 * half : 64 * half);
+          constexpr uint32_t kNext = SRC ? 0 : 128, kEight = SRC ? 512 : 1024;
+          const uint32_t odd = SRC ? at ^ 64 : at;
+          pair_rows<SRC>(at + 2 * sub * kEight, odd + kNext + 2 * sub * kEight, lo);
+          pair_rows<SRC>(at + (2 * sub + 1) * kEight, odd + kNext + (2 * sub + 1) * kEight, hi);
+          uint32_t p0 = 0, p1 = 0;
+          if (SRC) {
+            p0 = __shfl_sync(0xffffffffu, pow2[half], 16 * sub + 2 * t);
+            p1 = __shfl_sync(0xffffffffu, pow2[half], 16 * sub + 8 + 2 * t);
           }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const uint32_t b0 = SRC ? scale_pair(b[j][0], p0) : b[j][0], b1 = SRC ? scale_pair(b[j][1], p1) : b[j][1];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t a[4] = {lo[2 * i], lo[2 * i + 1], hi[2 * i], hi[2 * i + 1]};
+              mma_bf16(acc[2 * half + i][j], a, b0, b1);
+            }
+          }
+        }
+      }
     }
-    __syncthreads();
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  grid_dep_launch_dependents();
+
+  // the row warps' sums, up to 32 columns of S at a time: [row warps][columns of X][columns of S]; the result
+  // goes to [columns of X][NT * 8] behind them
+  constexpr int kJ = NT < 4 ? NT : 4;
+  const int cols = p.col_warps * kTileCols;
+  float* sums = reinterpret_cast<float*>(smem);
+  float* result = sums + kWarps * kTileCols * kJ * 8;
+#pragma unroll
+  for (int j0 = 0; j0 < NT; j0 += kJ) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int col = cw * kTileCols + (i >> 1) * 32 + 4 * g + 2 * (i & 1) + h;
+          *reinterpret_cast<float2*>(sums + (rw * cols + col) * kJ * 8 + j * 8 + 2 * t) =
+              make_float2(acc[i][j0 + j][2 * h], acc[i][j0 + j][2 * h + 1]);
+        }
+    __syncthreads();
+    for (int i = threadIdx.x * 4; i < cols * kJ * 8; i += kThreads * 4) {
+      float4 v = *reinterpret_cast<const float4*>(sums + i);
+      for (int w = 1; w < row_warps; ++w) {
+        const float4 a = *reinterpret_cast<const float4*>(sums + w * cols * kJ * 8 + i);
+        v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+      }
+      *reinterpret_cast<float4*>(result + i / (kJ * 8) * NT * 8 + j0 * 8 + i % (kJ * 8)) = v;
+    }
+  }
+  __syncthreads();
   float* out = p.out + static_cast<size_t>(blockIdx.y) * p.K * p.r;
-  for (int i = threadIdx.x; i < kCtaCols * NT * 8; i += kThreads) {
-    const int c = blockIdx.x * kCtaCols + i / (NT * 8), n = n0 + i % (NT * 8);
-    if (c < p.K && n < p.r) out[static_cast<size_t>(c) * p.r + n] = s_sum[i / (NT * 8)][i % (NT * 8)];
+  for (int i = threadIdx.x; i < cols * NT * 8; i += kThreads) {
+    const int k = blockIdx.x * cols + i / (NT * 8), n = n0 + i % (NT * 8);
+    if (k < p.K && n < p.r) out[static_cast<size_t>(k) * p.r + n] = result[i];
   }
 }
 
-__global__ void __launch_bounds__(256) wgrad_sum_kernel(const float* __restrict__ partial, int splits, size_t n,
+__global__ void __launch_bounds__(256) wgrad_sum_kernel(const float* __restrict__ partial, int parts, size_t n,
                                                      float* __restrict__ G) {
   const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+  grid_dep_wait();
   if (i >= n) return;
-  float s = partial[i];
-  for (int j = 1; j < splits; ++j) s += partial[j * n + i];
+  float s = 0.0f;
+  for (int j = 0; j < parts; j += 8) {  // eight loads in flight
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = j + e < parts ? partial[(j + e) * n + i] : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += v[e];
+  }
   G[i] = s;
 }
 
 struct Plan {
-  int nt, cols, zs, splits, steps;
+  int nt, col_warps, blocks, zs, parts, rows;
 };
 
-Plan plan(int M, int K, int r) {
+// One CTA of 16 warps per SM.  The column warps are as many as leave 18 column blocks, which 8 CTAs along the
+// rows make the whole device; the rows are split into as many parts as the device has room for, but no
+// warp sums more than kMaxRows into one accumulator.
+Plan plan(int M, int K, int r, int tile_rows) {
   Plan q{};
   const int tiles = (r + 7) / 8;
   q.nt = tiles <= 1 ? 1 : tiles <= 2 ? 2 : tiles <= 4 ? 4 : 8;
   q.zs = (tiles + q.nt - 1) / q.nt;
-  q.cols = (K + kCtaCols - 1) / kCtaCols;
-  const int all = (M + kCtaRows - 1) / kCtaRows;
-  // two CTAs per SM, and no accumulator over more than 20 steps (320 tokens a warp)
-  int splits = (2 * kSMs + q.cols * q.zs - 1) / (q.cols * q.zs);
-  if (splits * 20 < all) splits = (all + 19) / 20;
-  if (splits > all) splits = all;
-  q.steps = (all + splits - 1) / splits;
-  q.splits = (all + q.steps - 1) / q.steps;
+  q.col_warps = K >= 17 * 256 + 1 ? 4 : K >= 17 * 128 + 1 ? 2 : 1;
+  q.blocks = (K + q.col_warps * kTileCols - 1) / (q.col_warps * kTileCols);
+  const int block_rows = kWarps / q.col_warps * tile_rows, max_steps = kMaxRows / tile_rows;
+  const int steps = (M + block_rows - 1) / block_rows;
+  const int parts = std::max({1, std::min(kSMs / (q.blocks * q.zs), steps), (steps + max_steps - 1) / max_steps});
+  const int per_cta = (steps + parts - 1) / parts;
+  q.parts = (steps + per_cta - 1) / per_cta;
+  q.rows = per_cta * block_rows;
   return q;
 }
 
-template <int SRC>
+template <int SRC, int NT>
 svdq_status launch(const WgradParams& p, const Plan& q, cudaStream_t stream) {
-  const dim3 grid(q.cols, q.splits, q.zs);
-  switch (q.nt) {
-    case 1: wgrad_kernel<SRC, 1><<<grid, kThreads, 0, stream>>>(p); break;
-    case 2: wgrad_kernel<SRC, 2><<<grid, kThreads, 0, stream>>>(p); break;
-    case 4: wgrad_kernel<SRC, 4><<<grid, kThreads, 0, stream>>>(p); break;
-    default: wgrad_kernel<SRC, 8><<<grid, kThreads, 0, stream>>>(p); break;
-  }
+  constexpr int kJ = NT < 4 ? NT : 4;
+  const size_t loop = kSBytes + static_cast<size_t>(kWarps) * Tile<SRC>::stages * Tile<SRC>::bytes;
+  const size_t join = (static_cast<size_t>(kWarps) * kTileCols * kJ * 8 +
+                       static_cast<size_t>(q.col_warps) * kTileCols * NT * 8) * sizeof(float);
+  const size_t smem = std::max(loop, join);
+  SVDQ_CUDA_TRY(cudaFuncSetAttribute(wgrad_kernel<SRC, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(smem)));
+  wgrad_kernel<SRC, NT><<<dim3(q.blocks, q.parts, q.zs), kThreads, smem, stream>>>(p);
   SVDQ_CUDA_TRY(cudaGetLastError());
   return SVDQ_OK;
+}
+
+template <int SRC>
+svdq_status launch_nt(const WgradParams& p, const Plan& q, cudaStream_t stream) {
+  switch (q.nt) {
+    case 1: return launch<SRC, 1>(p, q, stream);
+    case 2: return launch<SRC, 2>(p, q, stream);
+    case 4: return launch<SRC, 4>(p, q, stream);
+    default: return launch<SRC, 8>(p, q, stream);
+  }
 }
 
 }  // namespace
 
 size_t lowrank_wgrad_workspace(int M, int K, int r) {
-  const Plan q = plan(M, K, r);
-  return q.splits > 1 ? static_cast<size_t>(q.splits) * K * r * sizeof(float) : 0;
+  const int parts = std::max(plan(M, K, r, Tile<0>::rows).parts, plan(M, K, r, Tile<1>::rows).parts);
+  return parts > 1 ? static_cast<size_t>(parts) * K * r * sizeof(float) : 0;
 }
 
 svdq_status launch_lowrank_wgrad(const void* X, const uint8_t* scales, int src, const void* S, int M, int K, int r,
                                  float* G, void* workspace, cudaStream_t stream) {
-  const Plan q = plan(M, K, r);
-  WgradParams p{X, scales, static_cast<const uint16_t*>(S), q.splits > 1 ? static_cast<float*>(workspace) : G,
-                M, K, r, q.steps};
-  SVDQ_TRY(src == 0 ? launch<0>(p, q, stream) : src == 1 ? launch<1>(p, q, stream) : launch<2>(p, q, stream));
-  if (q.splits > 1) {
+  const Plan q = plan(M, K, r, src ? Tile<1>::rows : Tile<0>::rows);
+  if (q.parts > 65535 || q.blocks > 0x7FFFFFFF / 8)
+    return fail(SVDQ_ERR_INVALID_ARG, "M=%d rows of K=%d are too many", M, K);
+  WgradParams p{static_cast<const uint8_t*>(X), scales, static_cast<const uint16_t*>(S),
+                q.parts > 1 ? static_cast<float*>(workspace) : G, M, K, r, q.col_warps, q.rows};
+  SVDQ_TRY(src == 0 ? launch_nt<0>(p, q, stream) : src == 1 ? launch_nt<1>(p, q, stream) : launch_nt<2>(p, q, stream));
+  if (q.parts > 1) {
     const size_t n = static_cast<size_t>(K) * r;
-    wgrad_sum_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, stream>>>(p.out, q.splits, n, G);
-    SVDQ_CUDA_TRY(cudaGetLastError());
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>((n + 255) / 256));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    SVDQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, wgrad_sum_kernel, static_cast<const float*>(p.out), q.parts, n, G));
   }
   return SVDQ_OK;
 }
