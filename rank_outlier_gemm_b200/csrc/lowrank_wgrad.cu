@@ -72,6 +72,17 @@ __device__ __forceinline__ uint32_t lds8(uint32_t at) {
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
   return v;
 }
+// (v & mask) | bits; `bits` from a register, so that it is one instruction
+__device__ __forceinline__ uint32_t mask_or(uint32_t v, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(bits));
+  return r;
+}
+__device__ __forceinline__ uint32_t opaque(uint32_t constant) {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %1;" : "=r"(r) : "r"(constant));
+  return r;
+}
 __device__ __forceinline__ uint32_t scale_pair(uint32_t values, uint32_t pow2) {
   const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&values),
                                    *reinterpret_cast<const __nv_bfloat162*>(&pow2));
@@ -102,18 +113,19 @@ __device__ __forceinline__ uint32_t s_place(int row, int j) {
 
 // Pairs over two rows of four columns of a tile: the words at `a` (one row) and `b` (the next).
 template <int SRC>
-__device__ __forceinline__ void pair_rows(uint32_t at_a, uint32_t at_b, uint32_t (&w)[4]) {
+__device__ __forceinline__ void pair_rows(uint32_t at_a, uint32_t at_b, uint32_t bf16_128, uint32_t (&w)[4]) {
   if (SRC == 0) {
     const uint2 a = lds64(at_a), b = lds64(at_b);
     w[0] = __byte_perm(a.x, b.x, 0x5410), w[1] = __byte_perm(a.x, b.x, 0x7632);
     w[2] = __byte_perm(a.y, b.y, 0x5410), w[3] = __byte_perm(a.y, b.y, 0x7632);
   } else if (SRC == 1) {
-    // u = q + 128 = 128 h + u7; bf16 has 7 mantissa bits: (128 + u7) - (256 - 128 h), exact, both rows at once
-    const uint32_t a = lds32(at_a) ^ 0x80808080u, b = lds32(at_b) ^ 0x80808080u;
+    // q = u7 - 128 s in two's complement; bf16 has 7 mantissa bits: (128 + u7) - (128 + 128 s), exact, both rows
+    // at once
+    const uint32_t a = lds32(at_a), b = lds32(at_b);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t v = __byte_perm(a, b, 0x4400 + 0x1111 * j);  // bytes j of a, -, j of b, -
-      const uint32_t u = (v & 0x007F007Fu) | 0x43004300u, c = (v & 0x00800080u) ^ 0x43804380u;
+      const uint32_t u = mask_or(v, 0x007F007Fu, bf16_128), c = mask_or(v, 0x00800080u, bf16_128);
       const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&c));
       w[j] = *reinterpret_cast<const uint32_t*>(&h);
     }
@@ -131,7 +143,7 @@ __device__ __forceinline__ void pair_rows(uint32_t at_a, uint32_t at_b, uint32_t
 
 // NT: columns of S per CTA in tiles of 8.  blockIdx: x columns of X, y CTA of the rows, z columns of S.
 template <int SRC, int NT>
-__global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
+__global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(WgradParams p) {
   extern __shared__ __align__(128) uint8_t smem[];  // S, then the rings; at the end the warps' sums
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -156,36 +168,47 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
   constexpr int kTileRows = Tl::rows, kStages = Tl::stages;
   constexpr int kRowsAtOnce = 32 / Tl::pieces;
   const int piece = lane % Tl::pieces, piece_k = k0 + piece * Tl::piece_values, fetch_row = lane / Tl::pieces;
-  const size_t row_bytes = static_cast<size_t>(p.K) * (SRC ? 1 : 2);
+  const size_t row_bytes = static_cast<size_t>(p.K) * (SRC ? 1 : 2), row_jump = kRowsAtOnce * row_bytes,
+               block_bytes = block_rows * row_bytes;
   const uint8_t* next_x = p.X + (row0 + rw * kTileRows + fetch_row) * row_bytes + static_cast<size_t>(piece_k) * (SRC ? 1 : 2);
   const uint8_t* next_s = SRC ? p.scales + static_cast<size_t>(row0 + rw * kTileRows + lane) * groups + k0 / kCkptGroup
                               : nullptr;
   const uint8_t* scales_end = SRC ? p.scales + static_cast<size_t>(p.M) * groups : nullptr;
+  const uint32_t fetch_at = Tl::at(fetch_row, piece);  // kRowsAtOnce rows on: 512 bytes on
   int fetch_left = piece_k < p.K ? row_end - row0 - rw * kTileRows : 0;  // rows from the tile's first to the end
   int scale_left = k0 < p.K ? row_end - row0 - rw * kTileRows - lane : 0;
+  // the rows whose aligned words (3 bytes before their first scale to 8 behind) lie inside the array
+  int scale_row = row0 + rw * kTileRows + lane;
+  const int scale_first = (3 + groups - 1) / groups, scale_last = p.M - (8 + k0 / kCkptGroup + groups - 1) / groups;
   auto fetch = [&](int stage) {
-    const uint32_t to = ring + stage * Tl::bytes;
+    const uint32_t to = ring + stage * Tl::bytes, at = to + fetch_at;
+    if (fetch_left >= kTileRows) {
+      const uint8_t* from = next_x;
 #pragma unroll
-    for (int i = 0; i < kTileRows / kRowsAtOnce; ++i) {
-      const int row = i * kRowsAtOnce + fetch_row;
-      const bool in = row < fetch_left;
-      copy16(to + Tl::at(row, piece), in ? next_x + i * kRowsAtOnce * row_bytes : p.X, in);
+      for (int i = 0; i < kTileRows / kRowsAtOnce; ++i, from += row_jump)
+        copy16(at + i * 512, from, true);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTileRows / kRowsAtOnce; ++i) {
+        const bool in = i * kRowsAtOnce + fetch_row < fetch_left;
+        copy16(at + i * 512, in ? next_x + i * row_jump : p.X, in);
+      }
     }
     if (SRC && scale_left > 0) {  // the aligned words around a row's scale bytes
       const uint32_t skip = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(next_s)) & 3;
       const uint8_t* word = next_s - skip;
-      const uint32_t at = to + Tl::scales + lane * 8 - s_tile;
-      if (word >= p.scales && word + (skip == 3 ? 8 : 4) <= scales_end) {
-        copy4_async(smem + at, word);
-        if (skip == 3) copy4_async(smem + at + 4, word + 4);
-      } else {  // the array's first or last bytes
+      uint8_t* here = smem + (to + Tl::scales + lane * 8 - s_tile);
+      if (scale_row >= scale_first && scale_row < scale_last) {
+        copy4_async(here, word);
+        if (skip == 3) copy4_async(here + 4, word + 4);  // each costs a sector of its own
+      } else {  // words that may reach over the array's ends
         for (int b = 0; b < 8; ++b)
-          if (word + b >= p.scales && word + b < scales_end) smem[at + b] = word[b];
+          if (word + b >= p.scales && word + b < scales_end) here[b] = word[b];
       }
     }
-    next_x += block_rows * row_bytes;
+    next_x += block_bytes;
     fetch_left -= block_rows;
-    if (SRC) next_s += static_cast<size_t>(block_rows) * groups, scale_left -= block_rows;
+    if (SRC) next_s += static_cast<size_t>(block_rows) * groups, scale_left -= block_rows, scale_row += block_rows;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   // where this lane finds rows 2 t (and, by other bits of the address, 2 t + 1, + 8, the second 32 columns)
@@ -194,6 +217,7 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
   // the scale bytes of row `lane` of a tile
   const uint32_t my_byte0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.scales)) + k0 / kCkptGroup;
   const bool second = k0 + 32 < p.K;  // the columns' second group exists
+  const uint32_t bf16_128 = opaque(0x43004300u);  // two bf16 of 128
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
@@ -202,13 +226,13 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
     const int n_rows = min(s_steps * block_rows, row_end - row);
     const int n_steps = (n_rows + block_rows - 1) / block_rows;
     __syncthreads();  // the rows of S before these are done with
-    const bool wide = p.r % 8 == 0;
-    for (int i = threadIdx.x; i < n_steps * block_rows * NT; i += kThreads) {
-      const int m = i / NT, j = i % NT, n = n0 + j * 8;
+    constexpr int kAtOnce = kThreads / NT;  // rows; a multiple of the placement's period
+    const int j = threadIdx.x % NT, n = n0 + j * 8;
+    const uint16_t* from = p.S + static_cast<size_t>(row + threadIdx.x / NT) * p.r + n;
+    uint32_t to = s_tile + s_place<NT>(threadIdx.x / NT, j);
+    for (int m = threadIdx.x / NT; m < n_steps * block_rows; m += kAtOnce, from += kAtOnce * p.r, to += kAtOnce * NT * 16) {
       const bool in = m < n_rows && n < p.r;
-      const uint16_t* from = p.S + static_cast<size_t>(row + m) * p.r + n;
-      const uint32_t to = s_tile + s_place<NT>(m, j);
-      if (wide) {
+      if (p.r % 8 == 0) {
         copy16(to, in ? from : p.S, in);
       } else {
         uint16_t* v = reinterpret_cast<uint16_t*>(smem + (to - s_tile));
@@ -263,8 +287,8 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
           const uint32_t at = (tile + x_at) ^ (SRC ? 32 * half : 64 * half);
           constexpr uint32_t kNext = SRC ? 0 : 128, kEight = SRC ? 512 : 1024;
           const uint32_t odd = SRC ? at ^ 64 : at;
-          pair_rows<SRC>(at + 2 * sub * kEight, odd + kNext + 2 * sub * kEight, lo);
-          pair_rows<SRC>(at + (2 * sub + 1) * kEight, odd + kNext + (2 * sub + 1) * kEight, hi);
+          pair_rows<SRC>(at + 2 * sub * kEight, odd + kNext + 2 * sub * kEight, bf16_128, lo);
+          pair_rows<SRC>(at + (2 * sub + 1) * kEight, odd + kNext + (2 * sub + 1) * kEight, bf16_128, hi);
           uint32_t p0 = 0, p1 = 0;
           if (SRC) {
             p0 = __shfl_sync(0xffffffffu, pow2[half], 16 * sub + 2 * t);
@@ -286,12 +310,12 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   grid_dep_launch_dependents();
 
-  // the row warps' sums, up to 32 columns of S at a time: [row warps][columns of X][columns of S]; the result
-  // goes to [columns of X][NT * 8] behind them
-  constexpr int kJ = NT < 4 ? NT : 4;
+  // the row warps' sums, up to 32 columns of S at a time: [row warps][columns of X][kPitch]; the pitch
+  // spreads a warp's stores over the banks
+  constexpr int kJ = NT < 4 ? NT : 4, kPitch = kJ * 8 + 2;
   const int cols = p.col_warps * kTileCols;
   float* sums = reinterpret_cast<float*>(smem);
-  float* result = sums + kWarps * kTileCols * kJ * 8;
+  float* out = p.out + static_cast<size_t>(blockIdx.y) * p.K * p.r;
 #pragma unroll
   for (int j0 = 0; j0 < NT; j0 += kJ) {
     __syncthreads();
@@ -302,24 +326,19 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradParams p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int col = cw * kTileCols + (i >> 1) * 32 + 4 * g + 2 * (i & 1) + h;
-          *reinterpret_cast<float2*>(sums + (rw * cols + col) * kJ * 8 + j * 8 + 2 * t) =
+          *reinterpret_cast<float2*>(sums + (rw * cols + col) * kPitch + j * 8 + 2 * t) =
               make_float2(acc[i][j0 + j][2 * h], acc[i][j0 + j][2 * h + 1]);
         }
     __syncthreads();
-    for (int i = threadIdx.x * 4; i < cols * kJ * 8; i += kThreads * 4) {
-      float4 v = *reinterpret_cast<const float4*>(sums + i);
-      for (int w = 1; w < row_warps; ++w) {
-        const float4 a = *reinterpret_cast<const float4*>(sums + w * cols * kJ * 8 + i);
-        v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
-      }
-      *reinterpret_cast<float4*>(result + i / (kJ * 8) * NT * 8 + j0 * 8 + i % (kJ * 8)) = v;
+    for (int i = threadIdx.x; i < cols * kJ * 8; i += kThreads) {
+      const int col = i / (kJ * 8), n = i % (kJ * 8);
+      const float* s = sums + col * kPitch + n;
+      float v = s[0];
+#pragma unroll 4
+      for (int w = 1; w < row_warps; ++w) v += s[w * cols * kPitch];
+      const int k = blockIdx.x * cols + col, c = n0 + j0 * 8 + n;
+      if (k < p.K && c < p.r) out[static_cast<size_t>(k) * p.r + c] = v;
     }
-  }
-  __syncthreads();
-  float* out = p.out + static_cast<size_t>(blockIdx.y) * p.K * p.r;
-  for (int i = threadIdx.x; i < cols * NT * 8; i += kThreads) {
-    const int k = blockIdx.x * cols + i / (NT * 8), n = n0 + i % (NT * 8);
-    if (k < p.K && n < p.r) out[static_cast<size_t>(k) * p.r + n] = result[i];
   }
 }
 
@@ -366,8 +385,7 @@ template <int SRC, int NT>
 svdq_status launch(const WgradParams& p, const Plan& q, cudaStream_t stream) {
   constexpr int kJ = NT < 4 ? NT : 4;
   const size_t loop = kSBytes + static_cast<size_t>(kWarps) * Tile<SRC>::stages * Tile<SRC>::bytes;
-  const size_t join = (static_cast<size_t>(kWarps) * kTileCols * kJ * 8 +
-                       static_cast<size_t>(q.col_warps) * kTileCols * NT * 8) * sizeof(float);
+  const size_t join = static_cast<size_t>(kWarps) * kTileCols * (kJ * 8 + 2) * sizeof(float);
   const size_t smem = std::max(loop, join);
   SVDQ_CUDA_TRY(cudaFuncSetAttribute(wgrad_kernel<SRC, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      static_cast<int>(smem)));
