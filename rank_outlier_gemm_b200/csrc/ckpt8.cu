@@ -27,46 +27,75 @@ __device__ __forceinline__ void split_index(uint64_t idx, uint64_t total, uint32
   }
 }
 
-// One thread per 8 values (vector) or per value (element); a group is 4 threads or a warp.
-template <typename T, int FMT, bool VEC>
+// Eight raw values of the vector layout.
+template <typename T>
+struct Raw8 {
+  uint4 w;
+  __device__ void load(const T* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ uint32_t largest() const { return largest8(w, static_cast<const T*>(nullptr)); }
+  __device__ void values(float (&v)[8]) const { unpack8(w, v, static_cast<const T*>(nullptr)); }
+};
+template <>
+struct Raw8<float> {
+  float f[8];
+  __device__ void load(const float* p) { load8(p, f); }
+  __device__ uint32_t largest() const { return largest8(f); }
+  __device__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = f[j];
+  }
+};
+
+// Vector layout: kUnroll chunks of 8 values per thread, a group is 4 neighbouring threads' chunks; their
+// loads are all in flight before the first is used.  Element layout: a value per thread, a group is a warp.
+constexpr int kUnroll = 4;
+template <typename T, int FMT>
 __global__ void __launch_bounds__(kThreads) ckpt_encode_kernel(const T* __restrict__ X, int64_t ld, uint64_t total,
                                                             uint32_t per_row, int K, uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales) {
+  const int groups = (K + kCkptGroup - 1) / kCkptGroup;
+  Raw8<T> raw[kUnroll];
+  uint64_t row[kUnroll];
+  uint32_t at[kUnroll];
+  bool in[kUnroll];
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    const uint64_t idx = (static_cast<uint64_t>(blockIdx.x) * kUnroll + i) * kThreads + threadIdx.x;
+    split_index(idx < total ? idx : total - 1, total, per_row, row[i], at[i]);
+    in[i] = idx < total && at[i] * 8 < static_cast<uint32_t>(K);
+    if (in[i]) raw[i].load(X + row[i] * ld + at[i] * 8);
+  }
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    uint32_t m = in[i] ? raw[i].largest() : 0u;
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const uint32_t b = ckpt_scale_byte<FMT>(m);
+    if (in[i]) {
+      float v[8];
+      raw[i].values(v);
+      *reinterpret_cast<uint2*>(codes + row[i] * K + at[i] * 8) =
+          make_uint2(ckpt_codes4<FMT>(v[0], v[1], v[2], v[3], b), ckpt_codes4<FMT>(v[4], v[5], v[6], v[7], b));
+      if (at[i] % 4 == 0) scales[row[i] * groups + at[i] / 4] = static_cast<uint8_t>(b);
+    }
+  }
+}
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads) ckpt_encode_element_kernel(const T* __restrict__ X, int64_t ld, uint64_t total,
+                                                                    uint32_t per_row, int K, uint8_t* __restrict__ codes,
+                                                                    uint8_t* __restrict__ scales) {
   const uint64_t idx = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
   uint64_t row = 0;
   uint32_t at = 0;
   split_index(idx < total ? idx : total - 1, total, per_row, row, at);
-  const int groups = (K + kCkptGroup - 1) / kCkptGroup;
-  const T* x = X + row * ld;
-  uint8_t* q = codes + row * K;
-  uint8_t* s = scales + row * groups;
-  if (VEC) {
-    const int c = static_cast<int>(at) * 8;
-    const bool in = idx < total && c < K;
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    if (in) load8(x + c, v);
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t b = ckpt_scale_byte<FMT>(m);
-    if (in) {
-      *reinterpret_cast<uint2*>(q + c) = make_uint2(ckpt_codes4<FMT>(v[0], v[1], v[2], v[3], b),
-                                                   ckpt_codes4<FMT>(v[4], v[5], v[6], v[7], b));
-      if (c % kCkptGroup == 0) s[c / kCkptGroup] = static_cast<uint8_t>(b);
-    }
-  } else {
-    const int c = static_cast<int>(at);
-    const bool in = idx < total && c < K;
-    const float v = in ? to_f32(x[c]) : 0.0f;
-    const uint32_t b = ckpt_scale_byte<FMT>(__reduce_max_sync(0xffffffffu, abs_bits(v)));
-    if (in) {
-      q[c] = static_cast<uint8_t>(ckpt_codes4<FMT>(v, 0.0f, 0.0f, 0.0f, b) & 0xFFu);
-      if (c % kCkptGroup == 0) s[c / kCkptGroup] = static_cast<uint8_t>(b);
-    }
+  const bool in = idx < total && at < static_cast<uint32_t>(K);
+  const float v = in ? to_f32(X[row * ld + at]) : 0.0f;
+  const uint32_t b = ckpt_scale_byte<FMT>(__reduce_max_sync(0xffffffffu, abs_bits(v)));
+  if (in) {
+    codes[row * K + at] = static_cast<uint8_t>(ckpt_codes4<FMT>(v, 0.0f, 0.0f, 0.0f, b) & 0xFFu);
+    if (at % kCkptGroup == 0)
+      scales[row * ((K + kCkptGroup - 1) / kCkptGroup) + at / kCkptGroup] = static_cast<uint8_t>(b);
   }
 }
 
@@ -98,11 +127,11 @@ struct Grid {
   unsigned blocks;
 };
 
-// Items of M rows, each row's padded to whole groups for the encoder (`pad` items).
-svdq_status item_grid(int M, int items, int pad, Grid* g) {
+// Items of M rows, each row's padded to whole groups for the encoder (`pad` items), `per_thread` a thread.
+svdq_status item_grid(int M, int items, int pad, int per_thread, Grid* g) {
   g->per_row = static_cast<uint32_t>(round_up(items, pad));
   g->total = static_cast<uint64_t>(M) * g->per_row;
-  const uint64_t blocks = (g->total + kThreads - 1) / kThreads;
+  const uint64_t blocks = (g->total + kThreads * per_thread - 1) / (kThreads * per_thread);
   if (blocks > 0x7FFFFFFFull) return fail(SVDQ_ERR_INVALID_ARG, "M=%d rows are too many", M);
   g->blocks = static_cast<unsigned>(blocks);
   return SVDQ_OK;
@@ -113,11 +142,11 @@ svdq_status encode(const void* X, int64_t ld, int M, int K, uint8_t* codes, uint
   Grid g;
   const T* x = static_cast<const T*>(X);
   if (K % 8 == 0 && ld % 8 == 0 && aligned16(X) && aligned16(codes)) {
-    SVDQ_TRY(item_grid(M, K / 8, 4, &g));
-    ckpt_encode_kernel<T, FMT, true><<<g.blocks, kThreads, 0, stream>>>(x, ld, g.total, g.per_row, K, codes, scales);
+    SVDQ_TRY(item_grid(M, K / 8, 4, kUnroll, &g));
+    ckpt_encode_kernel<T, FMT><<<g.blocks, kThreads, 0, stream>>>(x, ld, g.total, g.per_row, K, codes, scales);
   } else {
-    SVDQ_TRY(item_grid(M, K, kCkptGroup, &g));
-    ckpt_encode_kernel<T, FMT, false><<<g.blocks, kThreads, 0, stream>>>(x, ld, g.total, g.per_row, K, codes, scales);
+    SVDQ_TRY(item_grid(M, K, kCkptGroup, 1, &g));
+    ckpt_encode_element_kernel<T, FMT><<<g.blocks, kThreads, 0, stream>>>(x, ld, g.total, g.per_row, K, codes, scales);
   }
   SVDQ_CUDA_TRY(cudaGetLastError());
   return SVDQ_OK;
@@ -128,10 +157,10 @@ svdq_status decode(const uint8_t* codes, const uint8_t* scales, int M, int K, vo
   Grid g;
   T* x = static_cast<T*>(X);
   if (K % 8 == 0 && ld % 8 == 0 && aligned16(X) && aligned16(codes)) {
-    SVDQ_TRY(item_grid(M, K / 8, 1, &g));
+    SVDQ_TRY(item_grid(M, K / 8, 1, 1, &g));
     ckpt_decode_kernel<T, FMT, true><<<g.blocks, kThreads, 0, stream>>>(codes, scales, g.total, g.per_row, K, x, ld);
   } else {
-    SVDQ_TRY(item_grid(M, K, 1, &g));
+    SVDQ_TRY(item_grid(M, K, 1, 1, &g));
     ckpt_decode_kernel<T, FMT, false><<<g.blocks, kThreads, 0, stream>>>(codes, scales, g.total, g.per_row, K, x, ld);
   }
   SVDQ_CUDA_TRY(cudaGetLastError());

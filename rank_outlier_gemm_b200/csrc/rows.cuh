@@ -201,16 +201,19 @@ template <int FMT>
 __device__ __forceinline__ uint32_t ckpt_codes4(float a, float b, float c, float d, uint32_t byte) {
   if (byte == 0xFFu) return 0u;  // a NaN or an infinity in the group
   const float inv = __uint_as_float((254u - byte) << 23);
-  a *= inv, b *= inv, c *= inv, d *= inv;
   if (FMT == SVDQ_CKPT8_INT8) {
     if (byte == 248u) {  // the largest scale: magnitudes up to 128
-      a = fminf(fmaxf(a, -127.0f), 127.0f), b = fminf(fmaxf(b, -127.0f), 127.0f);
-      c = fminf(fmaxf(c, -127.0f), 127.0f), d = fminf(fmaxf(d, -127.0f), 127.0f);
+      const float top = 127.0f / inv;
+      a = fminf(fmaxf(a, -top), top), b = fminf(fmaxf(b, -top), top);
+      c = fminf(fmaxf(c, -top), top), d = fminf(fmaxf(d, -top), top);
     }
-    const uint32_t lo = __byte_perm(__float2int_rn(a), __float2int_rn(b), 0x0040);
-    const uint32_t hi = __byte_perm(__float2int_rn(c), __float2int_rn(d), 0x0040);
+    // + 1.5 2^23: the rounded integer is in the low mantissa bits, as two's complement
+    constexpr float kMagic = 12582912.0f;
+    const uint32_t lo = __byte_perm(__float_as_uint(__fmaf_rn(a, inv, kMagic)), __float_as_uint(__fmaf_rn(b, inv, kMagic)), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(__fmaf_rn(c, inv, kMagic)), __float_as_uint(__fmaf_rn(d, inv, kMagic)), 0x0040);
     return __byte_perm(lo, hi, 0x5410);
   }
+  a *= inv, b *= inv, c *= inv, d *= inv;
   uint16_t lo, hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
@@ -258,15 +261,36 @@ __device__ __forceinline__ void ckpt_codes8_pairs(uint2 q, F2 (&v)[4]) {
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
+// The bits, as fp32, of the largest magnitude of eight values; a NaN counts as the largest.
+__device__ __forceinline__ uint32_t largest8(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+  return m;
+}
+__device__ __forceinline__ uint32_t largest8(const uint4& w, const __nv_bfloat16*) {
+  uint32_t m = w.x & 0x7FFF7FFFu;
+  const uint32_t r[3] = {w.y & 0x7FFF7FFFu, w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu};
+#pragma unroll
+  for (int j = 0; j < 3; ++j) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(r[j]));
+  return max(m << 16, m & 0xFFFF0000u);  // a NaN's bits are above an infinity's
+}
+__device__ __forceinline__ uint32_t largest8(const uint4& w, const __half*) {
+  uint32_t m = w.x & 0x7FFF7FFFu;
+  const uint32_t r[3] = {w.y & 0x7FFF7FFFu, w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu};
+#pragma unroll
+  for (int j = 0; j < 3; ++j) asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m) : "r"(r[j]));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+  return max(abs_bits(f.x), abs_bits(f.y));
+}
+
 // Writes chunk i of a row's checkpoint: codes (K bytes) and scales (ceil(K / 32) bytes).  Every lane
 // of the warp calls it; columns beyond K hold 0.
 template <int FMT, bool VEC>
 __device__ __forceinline__ void ckpt_store_chunk(uint8_t* codes, uint8_t* scales, int K, int i, int t, int threads,
                                                  const float (&v)[8]) {
   if (VEC) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+    uint32_t m = largest8(v);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const uint32_t b = ckpt_scale_byte<FMT>(m);
