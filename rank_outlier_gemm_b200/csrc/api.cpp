@@ -80,6 +80,16 @@ svdq_status check_device() {
   return SVDQ_OK;
 }
 
+svdq_status allow_dynamic_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  SVDQ_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return fail(SVDQ_ERR_UNSUPPORTED_DEVICE, "device index %d", dev);
+  if (done.load(std::memory_order_acquire) >> dev & 1) return SVDQ_OK;
+  SVDQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  done.fetch_or(1ull << dev, std::memory_order_release);
+  return SVDQ_OK;
+}
+
 svdq_status make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, uint64_t inner,
                          uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
                          CUtensorMapSwizzle swizzle) {

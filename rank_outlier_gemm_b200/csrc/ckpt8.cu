@@ -27,25 +27,6 @@ __device__ __forceinline__ void split_index(uint64_t idx, uint64_t total, uint32
   }
 }
 
-// Eight raw values of the vector layout.
-template <typename T>
-struct Raw8 {
-  uint4 w;
-  __device__ void load(const T* p) { w = *reinterpret_cast<const uint4*>(p); }
-  __device__ uint32_t largest() const { return largest8(w, static_cast<const T*>(nullptr)); }
-  __device__ void values(float (&v)[8]) const { unpack8(w, v, static_cast<const T*>(nullptr)); }
-};
-template <>
-struct Raw8<float> {
-  float f[8];
-  __device__ void load(const float* p) { load8(p, f); }
-  __device__ uint32_t largest() const { return largest8(f); }
-  __device__ void values(float (&v)[8]) const {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = f[j];
-  }
-};
-
 // Vector layout: kUnroll chunks of 8 values per thread, a group is 4 neighbouring threads' chunks; their
 // loads are all in flight before the first is used.  Element layout: a value per thread, a group is a warp.
 constexpr int kUnroll = 4;

@@ -12,6 +12,7 @@
 // second kernel adds them in a fixed order (no atomics: equal calls give equal bits).
 #include <algorithm>
 #include <initializer_list>
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "rows.cuh"
@@ -69,7 +70,23 @@ struct FwdParams {
   float eps, one;
 };
 
-template <typename T, int NV, bool VEC>
+// A chunk of a row as it was read: packed where the vector layout reads it so.
+template <typename T, bool VEC>
+struct Held : Raw8<T> {};
+template <typename T>
+struct Held<T, false> : Raw8<float> {};
+
+// A chunk of the per-group vectors.  P: their type where it is known (vector layout), void where it is not.
+template <typename P, bool VEC>
+__device__ __forceinline__ void param_chunk(const void* p, int dtype, size_t offset, int K, int i, int t, int threads,
+                                            float (&v)[8]) {
+  if constexpr (std::is_void<P>::value)
+    load_param_chunk<VEC>(p, dtype, offset, K, i, t, threads, 0.0f, v);
+  else
+    load8(static_cast<const P*>(p) + offset + row_column<true>(i, 0, t, threads), v);
+}
+
+template <typename T, typename P, int NV, bool VEC>
 __global__ void __launch_bounds__(512) layer_norm_kernel(FwdParams p) {
   __shared__ float red[kForwardWarps][64];
   const int threads = p.warps * 32, team = threadIdx.x / threads, t = threadIdx.x % threads;
@@ -77,52 +94,76 @@ __global__ void __launch_bounds__(512) layer_norm_kernel(FwdParams p) {
   if (m >= p.M) return;  // whole teams: a barrier has all of its team's warps
   int turn = 0;
   const T* z = static_cast<const T*>(p.Z) + m * p.ld_z;
-  float v[NV][8];
-  float sum = 0.0f;
+  Held<T, VEC> held[NV];
+  auto inside = [&](int i) { return !VEC || row_column<true>(i, 0, t, threads) < p.K; };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    load_chunk<T, VEC>(z, p.K, i, t, threads, 0.0f, v[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum += v[i][j];
-  }
-  if (p.ckpt >= 0) {
-    uint8_t* codes = p.codes + static_cast<size_t>(m) * p.K;
-    uint8_t* scales = p.scales + static_cast<size_t>(m) * ((p.K + kCkptGroup - 1) / kCkptGroup);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (p.ckpt == SVDQ_CKPT8_INT8)
-        ckpt_store_chunk<SVDQ_CKPT8_INT8, VEC>(codes, scales, p.K, i, t, threads, v[i]);
-      else
-        ckpt_store_chunk<SVDQ_CKPT8_E4M3, VEC>(codes, scales, p.K, i, t, threads, v[i]);
+    if constexpr (VEC) {
+      held[i].clear();
+      if (inside(i)) held[i].load(z + row_column<true>(i, 0, t, threads));
+    } else {
+      load_chunk<T, false>(z, p.K, i, t, threads, 0.0f, held[i].f);
     }
   }
+  F2 sum = f2(0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float v[8];
+    held[i].values(v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum = add2(sum, f2(v[2 * j], v[2 * j + 1]));
+  }
+  float s0, s1;
+  unpack2(sum, s0, s1);
   const float inv_k = 1.0f / static_cast<float>(p.K);
-  const float mu = team_sum(sum, p.warps, team, red[team], turn) * inv_k;
-  float sq = 0.0f;
+  const float mu = team_sum(s0 + s1, p.warps, team, red[team], turn) * inv_k;
+  F2 sq = f2(0.0f, 0.0f);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
+    if (!inside(i)) continue;
+    float v[8];
+    held[i].values(v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[i][j] -= mu;
-      if (row_column<VEC>(i, j, t, threads) < p.K) sq = __fmaf_rn(v[i][j], v[i][j], sq);
+    for (int j = 0; j < 8; ++j)
+      if (!VEC && row_column<false>(i, j, t, threads) >= p.K) v[j] = mu;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const F2 d = add2(f2(v[2 * j], v[2 * j + 1]), f2(-mu, -mu));
+      sq = fma2(d, d, sq);
     }
   }
-  const float var = team_sum(sq, p.warps, team, red[team], turn) * inv_k;
+  unpack2(sq, s0, s1);
+  const float var = team_sum(s0 + s1, p.warps, team, red[team], turn) * inv_k;
   const float rstd = __frcp_rn(__fsqrt_rn(__fadd_rn(var, p.eps)));
   if (p.stats && t == 0) p.stats[m] = make_float2(mu, rstd);
   const size_t group = static_cast<size_t>(m / p.rows) * p.ld_param;
   T* y = static_cast<T*>(p.Y) + m * p.ld_y;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    float a[8], c[8];
-    if (p.scale) load_param_chunk<VEC>(p.scale, p.param_dtype, group, p.K, i, t, threads, 0.0f, a);
-    if (p.shift) load_param_chunk<VEC>(p.shift, p.param_dtype, group, p.K, i, t, threads, 0.0f, c);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float xh = v[i][j] * rstd;
-      v[i][j] = __fmaf_rn(xh, p.scale ? a[j] + p.one : 1.0f, p.shift ? c[j] : 0.0f);
+    float v[8], a[8], c[8];
+    held[i].values(v);
+    const bool in = inside(i);
+    if (p.scale && in) param_chunk<P, VEC>(p.scale, p.param_dtype, group, p.K, i, t, threads, a);
+    if (p.shift && in) param_chunk<P, VEC>(p.shift, p.param_dtype, group, p.K, i, t, threads, c);
+    if (p.ckpt >= 0) {
+      uint8_t* codes = p.codes + static_cast<size_t>(m) * p.K;
+      uint8_t* scales = p.scales + static_cast<size_t>(m) * ((p.K + kCkptGroup - 1) / kCkptGroup);
+      const uint32_t top = VEC ? held[i].largest() : 0u;
+      if (p.ckpt == SVDQ_CKPT8_INT8)
+        ckpt_store_chunk<SVDQ_CKPT8_INT8, VEC>(codes, scales, p.K, i, t, threads, top, v);
+      else
+        ckpt_store_chunk<SVDQ_CKPT8_E4M3, VEC>(codes, scales, p.K, i, t, threads, top, v);
     }
-    store_chunk<T, VEC>(y, p.K, i, t, threads, v[i]);
+    if (!in) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // (z - mu) rstd in two steps: a row without variance gives exact zeros
+      F2 r = mul2(add2(f2(v[2 * j], v[2 * j + 1]), f2(-mu, -mu)), f2(rstd, rstd));
+      if (p.scale) r = mul2(r, add2(f2(a[2 * j], a[2 * j + 1]), f2(p.one, p.one)));
+      if (p.shift) r = add2(r, f2(c[2 * j], c[2 * j + 1]));
+      unpack2(r, v[2 * j], v[2 * j + 1]);
+    }
+    store_chunk<T, VEC>(y, p.K, i, t, threads, v);
   }
 }
 
@@ -506,23 +547,32 @@ int backward_splits(int K, int rows, int groups) {
   return want < most ? want : most;
 }
 
-template <typename T, int NV, bool VEC>
+template <typename T, typename P, int NV, bool VEC>
 svdq_status run_forward(const FwdParams& p, const Shape& s, cudaStream_t stream) {
   const int blocks = (p.M + s.teams - 1) / s.teams;
-  layer_norm_kernel<T, NV, VEC><<<blocks, s.teams * s.warps * 32, 0, stream>>>(p);
+  layer_norm_kernel<T, P, NV, VEC><<<blocks, s.teams * s.warps * 32, 0, stream>>>(p);
   SVDQ_CUDA_TRY(cudaGetLastError());
   return SVDQ_OK;
 }
 
-template <typename T, bool VEC>
+template <typename T, typename P, bool VEC>
 svdq_status forward_nv(const FwdParams& p, const Shape& s, cudaStream_t stream) {
   switch (s.nv) {
-    case 1: return run_forward<T, 1, VEC>(p, s, stream);
-    case 2: return run_forward<T, 2, VEC>(p, s, stream);
-    case 3: return run_forward<T, 3, VEC>(p, s, stream);
-    case 4: return run_forward<T, 4, VEC>(p, s, stream);
-    default: return run_forward<T, 5, VEC>(p, s, stream);
+    case 1: return run_forward<T, P, 1, VEC>(p, s, stream);
+    case 2: return run_forward<T, P, 2, VEC>(p, s, stream);
+    case 3: return run_forward<T, P, 3, VEC>(p, s, stream);
+    case 4: return run_forward<T, P, 4, VEC>(p, s, stream);
+    default: return run_forward<T, P, 5, VEC>(p, s, stream);
   }
+}
+
+// The parameters' type is compiled in where it is the rows' own or fp32.
+template <typename T>
+svdq_status forward_type(const FwdParams& p, const Shape& s, bool vec, int dtype, cudaStream_t stream) {
+  if (!vec) return forward_nv<T, void, false>(p, s, stream);
+  if (p.param_dtype == SVDQ_DTYPE_FP32) return forward_nv<T, float, true>(p, s, stream);
+  if (p.param_dtype == dtype) return forward_nv<T, T, true>(p, s, stream);
+  return forward_nv<T, void, true>(p, s, stream);
 }
 
 template <typename T, int NV, bool VEC, int SRC>
@@ -542,8 +592,8 @@ svdq_status run_backward(BwdParams p, const Shape& s, int groups, cudaStream_t s
   if (!p.err) return fail(SVDQ_ERR_CUDA, "device error word unavailable");
   p.wait_ns = wait_limit_ns();
   auto* kernel = layer_norm_backward_kernel<T, NV, VEC, SRC>;
-  if (smem > 40 * 1024)  // beside the static arrays
-    SVDQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem));
+  static std::atomic<uint64_t> allowed{0};
+  SVDQ_TRY(allow_dynamic_smem(reinterpret_cast<const void*>(kernel), kMaxSmem, allowed));
   kernel<<<groups * p.splits, (s.teams * s.warps + (VEC ? 1 : 0)) * 32, smem, stream>>>(p);
   SVDQ_CUDA_TRY(cudaGetLastError());
   return SVDQ_OK;
@@ -594,11 +644,9 @@ svdq_status launch_layer_norm(const NormArgs& a, const void* Z, const void* scal
   p.warps = s.warps;
   const bool vec = vector_rows(a.K, {Z, scale, shift, Y, codes}, {a.ld_z, a.ld_y, a.ld_param});
   switch (a.dtype) {
-    case SVDQ_DTYPE_BF16:
-      return vec ? forward_nv<__nv_bfloat16, true>(p, s, stream) : forward_nv<__nv_bfloat16, false>(p, s, stream);
-    case SVDQ_DTYPE_FP16:
-      return vec ? forward_nv<__half, true>(p, s, stream) : forward_nv<__half, false>(p, s, stream);
-    default: return vec ? forward_nv<float, true>(p, s, stream) : forward_nv<float, false>(p, s, stream);
+    case SVDQ_DTYPE_BF16: return forward_type<__nv_bfloat16>(p, s, vec, a.dtype, stream);
+    case SVDQ_DTYPE_FP16: return forward_type<__half>(p, s, vec, a.dtype, stream);
+    default: return forward_type<float>(p, s, vec, a.dtype, stream);
   }
 }
 

@@ -30,6 +30,7 @@ namespace {
 using namespace dev;
 
 constexpr int kSMs = 148;
+constexpr int kMaxSmem = 112 * 1024;  // two CTAs per SM at least
 constexpr int kMaxTokens = 16;
 constexpr int kPrepWarps = 16, kPrepThreads = 32 * kPrepWarps;
 constexpr int kStep = 128;        // weights of a row per warp step: 4 lanes x 32
@@ -536,8 +537,8 @@ svdq_status launch_main(W4A16Params& p, cudaStream_t stream) {
   // as many CTAs as the SMs hold at a time, so that the units are dealt out evenly
   const int resident = kSMs * (NT > 2 ? 2 : 3);
   const int grid = p.cluster > 1 || p.blocks < resident ? p.blocks : resident;
-  SVDQ_CUDA_TRY(cudaFuncSetAttribute(w4a16_kernel<INT4, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(smem)));
+  static std::atomic<uint64_t> allowed{0};
+  SVDQ_TRY(allow_dynamic_smem(reinterpret_cast<const void*>(w4a16_kernel<INT4, NT>), kMaxSmem, allowed));
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -387,8 +387,8 @@ svdq_status launch(const WgradParams& p, const Plan& q, cudaStream_t stream) {
   const size_t loop = kSBytes + static_cast<size_t>(kWarps) * Tile<SRC>::stages * Tile<SRC>::bytes;
   const size_t join = static_cast<size_t>(kWarps) * kTileCols * (kJ * 8 + 2) * sizeof(float);
   const size_t smem = std::max(loop, join);
-  SVDQ_CUDA_TRY(cudaFuncSetAttribute(wgrad_kernel<SRC, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(smem)));
+  static std::atomic<uint64_t> allowed{0};
+  SVDQ_TRY(allow_dynamic_smem(reinterpret_cast<const void*>(wgrad_kernel<SRC, NT>), static_cast<int>(smem), allowed));
   wgrad_kernel<SRC, NT><<<dim3(q.blocks, q.parts, q.zs), kThreads, smem, stream>>>(p);
   SVDQ_CUDA_TRY(cudaGetLastError());
   return SVDQ_OK;

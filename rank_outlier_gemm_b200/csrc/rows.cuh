@@ -284,14 +284,37 @@ __device__ __forceinline__ uint32_t largest8(const uint4& w, const __half*) {
   return max(abs_bits(f.x), abs_bits(f.y));
 }
 
+// Eight raw values of the vector layout.
+template <typename T>
+struct Raw8 {
+  uint4 w;
+  __device__ __forceinline__ void clear() { w = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ uint32_t largest() const { return largest8(w, static_cast<const T*>(nullptr)); }
+  __device__ __forceinline__ void values(float (&v)[8]) const { unpack8(w, v, static_cast<const T*>(nullptr)); }
+};
+template <>
+struct Raw8<float> {
+  float f[8];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+  }
+  __device__ __forceinline__ void load(const float* p) { load8(p, f); }
+  __device__ __forceinline__ uint32_t largest() const { return largest8(f); }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = f[j];
+  }
+};
+
 // Writes chunk i of a row's checkpoint: codes (K bytes) and scales (ceil(K / 32) bytes).  Every lane
-// of the warp calls it; columns beyond K hold 0.
+// of the warp calls it; columns beyond K hold 0 (`top`: the vector layout's largest magnitude).
 template <int FMT, bool VEC>
 __device__ __forceinline__ void ckpt_store_chunk(uint8_t* codes, uint8_t* scales, int K, int i, int t, int threads,
-                                                 const float (&v)[8]) {
+                                                 uint32_t top, const float (&v)[8]) {
   if (VEC) {
-    uint32_t m = largest8(v);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    uint32_t m = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const uint32_t b = ckpt_scale_byte<FMT>(m);
     const int c = row_column<true>(i, 0, t, threads);

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 #include <vector>
 
@@ -38,6 +39,10 @@ int* noalloc_error_word_if_ready();
 uint64_t wait_limit_ns();
 // SVDQ_OK if the current device is sm_100, else SVDQ_ERR_UNSUPPORTED_DEVICE.
 svdq_status check_device();
+
+// Lets `kernel` use up to `bytes` of dynamic shared memory on the current device; `done` (one per kernel)
+// has a bit per device where that has been said before.
+svdq_status allow_dynamic_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 // 2-D tiled tensor map over a row-major [outer, inner] array.
 svdq_status make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
