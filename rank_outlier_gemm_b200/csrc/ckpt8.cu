@@ -27,15 +27,15 @@ __device__ __forceinline__ void split_index(uint64_t idx, uint64_t total, uint32
   }
 }
 
-// Vector layout: kUnroll chunks of 8 values per thread, a group is 4 neighbouring threads' chunks; their
-// loads are all in flight before the first is used.  Element layout: a value per thread, a group is a warp.
+// kUnroll chunks of 8 values per thread, a group is 4 neighbouring threads' chunks; the chunks' loads are all
+// in flight before the first is used.
 constexpr int kUnroll = 4;
-template <typename T, int FMT>
+template <typename T, int FMT, bool VEC>
 __global__ void __launch_bounds__(kThreads) ckpt_encode_kernel(const T* __restrict__ X, int64_t ld, uint64_t total,
                                                             uint32_t per_row, int K, uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales) {
   const int groups = (K + kCkptGroup - 1) / kCkptGroup;
-  Raw8<T> raw[kUnroll];
+  Held<T, VEC> held[kUnroll];
   uint64_t row[kUnroll];
   uint32_t at[kUnroll];
   bool in[kUnroll];
@@ -43,40 +43,28 @@ __global__ void __launch_bounds__(kThreads) ckpt_encode_kernel(const T* __restri
   for (int i = 0; i < kUnroll; ++i) {
     const uint64_t idx = (static_cast<uint64_t>(blockIdx.x) * kUnroll + i) * kThreads + threadIdx.x;
     split_index(idx < total ? idx : total - 1, total, per_row, row[i], at[i]);
-    in[i] = idx < total && at[i] * 8 < static_cast<uint32_t>(K);
-    if (in[i]) raw[i].load(X + row[i] * ld + at[i] * 8);
+    at[i] *= 8;  // column
+    in[i] = idx < total && at[i] < static_cast<uint32_t>(K);
+    held[i].clear();
+    if (in[i]) {
+      const T* x = X + row[i] * ld + at[i];
+      if constexpr (VEC)
+        held[i].load(x);
+      else
+        load_any(x, min(8, K - static_cast<int>(at[i])), 0.0f, held[i].f);
+    }
   }
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
-    uint32_t m = in[i] ? raw[i].largest() : 0u;
+    uint32_t m = in[i] ? held[i].largest() : 0u;
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t b = ckpt_scale_byte<FMT>(m);
     if (in[i]) {
       float v[8];
-      raw[i].values(v);
-      *reinterpret_cast<uint2*>(codes + row[i] * K + at[i] * 8) =
-          make_uint2(ckpt_codes4<FMT>(v[0], v[1], v[2], v[3], b), ckpt_codes4<FMT>(v[4], v[5], v[6], v[7], b));
-      if (at[i] % 4 == 0) scales[row[i] * groups + at[i] / 4] = static_cast<uint8_t>(b);
+      held[i].values(v);
+      ckpt_store_codes<FMT, VEC>(codes + row[i] * K, scales + row[i] * groups, static_cast<int>(at[i]), K,
+                                 ckpt_scale_byte<FMT>(m), v);
     }
-  }
-}
-
-template <typename T, int FMT>
-__global__ void __launch_bounds__(kThreads) ckpt_encode_element_kernel(const T* __restrict__ X, int64_t ld, uint64_t total,
-                                                                    uint32_t per_row, int K, uint8_t* __restrict__ codes,
-                                                                    uint8_t* __restrict__ scales) {
-  const uint64_t idx = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  uint64_t row = 0;
-  uint32_t at = 0;
-  split_index(idx < total ? idx : total - 1, total, per_row, row, at);
-  const bool in = idx < total && at < static_cast<uint32_t>(K);
-  const float v = in ? to_f32(X[row * ld + at]) : 0.0f;
-  const uint32_t b = ckpt_scale_byte<FMT>(__reduce_max_sync(0xffffffffu, abs_bits(v)));
-  if (in) {
-    codes[row * K + at] = static_cast<uint8_t>(ckpt_codes4<FMT>(v, 0.0f, 0.0f, 0.0f, b) & 0xFFu);
-    if (at % kCkptGroup == 0)
-      scales[row * ((K + kCkptGroup - 1) / kCkptGroup) + at / kCkptGroup] = static_cast<uint8_t>(b);
   }
 }
 
@@ -89,17 +77,10 @@ __global__ void __launch_bounds__(kThreads) ckpt_decode_kernel(const uint8_t* __
   uint64_t row = 0;
   uint32_t at = 0;
   split_index(idx, total, per_row, row, at);
-  const int groups = (K + kCkptGroup - 1) / kCkptGroup;
-  const uint8_t* q = codes + row * K;
-  const uint8_t* s = scales + row * groups;
   float v[8];
-  if (VEC) {
-    ckpt_load_chunk<FMT, true>(q, s, K, 0, static_cast<int>(at), 0, v);
-    store8(X + row * ld + at * 8, v);
-  } else {
-    ckpt_values4<FMT>(q[at], ckpt_scale(s[at / kCkptGroup]), v);
-    X[row * ld + at] = from_f32<T>(v[0]);
-  }
+  ckpt_load_chunk<FMT, VEC>(codes + row * K, scales + row * ((K + kCkptGroup - 1) / kCkptGroup), K, 0,
+                            static_cast<int>(at), 0, v);
+  store_chunk<T, VEC>(X + row * ld, K, 0, static_cast<int>(at), 0, v);
 }
 
 struct Grid {
@@ -122,13 +103,11 @@ template <typename T, int FMT>
 svdq_status encode(const void* X, int64_t ld, int M, int K, uint8_t* codes, uint8_t* scales, cudaStream_t stream) {
   Grid g;
   const T* x = static_cast<const T*>(X);
-  if (K % 8 == 0 && ld % 8 == 0 && aligned16(X) && aligned16(codes)) {
-    SVDQ_TRY(item_grid(M, K / 8, 4, kUnroll, &g));
-    ckpt_encode_kernel<T, FMT><<<g.blocks, kThreads, 0, stream>>>(x, ld, g.total, g.per_row, K, codes, scales);
-  } else {
-    SVDQ_TRY(item_grid(M, K, kCkptGroup, 1, &g));
-    ckpt_encode_element_kernel<T, FMT><<<g.blocks, kThreads, 0, stream>>>(x, ld, g.total, g.per_row, K, codes, scales);
-  }
+  SVDQ_TRY(item_grid(M, (K + 7) / 8, 4, kUnroll, &g));
+  if (K % 8 == 0 && ld % 8 == 0 && aligned16(X))
+    ckpt_encode_kernel<T, FMT, true><<<g.blocks, kThreads, 0, stream>>>(x, ld, g.total, g.per_row, K, codes, scales);
+  else
+    ckpt_encode_kernel<T, FMT, false><<<g.blocks, kThreads, 0, stream>>>(x, ld, g.total, g.per_row, K, codes, scales);
   SVDQ_CUDA_TRY(cudaGetLastError());
   return SVDQ_OK;
 }
@@ -137,13 +116,11 @@ template <typename T, int FMT>
 svdq_status decode(const uint8_t* codes, const uint8_t* scales, int M, int K, void* X, int64_t ld, cudaStream_t stream) {
   Grid g;
   T* x = static_cast<T*>(X);
-  if (K % 8 == 0 && ld % 8 == 0 && aligned16(X) && aligned16(codes)) {
-    SVDQ_TRY(item_grid(M, K / 8, 1, 1, &g));
+  SVDQ_TRY(item_grid(M, (K + 7) / 8, 1, 1, &g));
+  if (K % 8 == 0 && ld % 8 == 0 && aligned16(X))
     ckpt_decode_kernel<T, FMT, true><<<g.blocks, kThreads, 0, stream>>>(codes, scales, g.total, g.per_row, K, x, ld);
-  } else {
-    SVDQ_TRY(item_grid(M, K, 1, 1, &g));
+  else
     ckpt_decode_kernel<T, FMT, false><<<g.blocks, kThreads, 0, stream>>>(codes, scales, g.total, g.per_row, K, x, ld);
-  }
   SVDQ_CUDA_TRY(cudaGetLastError());
   return SVDQ_OK;
 }

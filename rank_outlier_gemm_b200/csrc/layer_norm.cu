@@ -70,12 +70,6 @@ struct FwdParams {
   float eps, one;
 };
 
-// A chunk of a row as it was read: packed where the vector layout reads it so.
-template <typename T, bool VEC>
-struct Held : Raw8<T> {};
-template <typename T>
-struct Held<T, false> : Raw8<float> {};
-
 // A chunk of the per-group vectors.  P: their type where it is known (vector layout), void where it is not.
 template <typename P, bool VEC>
 __device__ __forceinline__ void param_chunk(const void* p, int dtype, size_t offset, int K, int i, int t, int threads,
@@ -83,7 +77,7 @@ __device__ __forceinline__ void param_chunk(const void* p, int dtype, size_t off
   if constexpr (std::is_void<P>::value)
     load_param_chunk<VEC>(p, dtype, offset, K, i, t, threads, 0.0f, v);
   else
-    load8(static_cast<const P*>(p) + offset + row_column<true>(i, 0, t, threads), v);
+    load8(static_cast<const P*>(p) + offset + chunk_column(i, t, threads), v);
 }
 
 template <typename T, typename P, int NV, bool VEC>
@@ -95,12 +89,12 @@ __global__ void __launch_bounds__(512) layer_norm_kernel(FwdParams p) {
   int turn = 0;
   const T* z = static_cast<const T*>(p.Z) + m * p.ld_z;
   Held<T, VEC> held[NV];
-  auto inside = [&](int i) { return !VEC || row_column<true>(i, 0, t, threads) < p.K; };
+  auto inside = [&](int i) { return chunk_column(i, t, threads) < p.K; };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     if constexpr (VEC) {
       held[i].clear();
-      if (inside(i)) held[i].load(z + row_column<true>(i, 0, t, threads));
+      if (inside(i)) held[i].load(z + chunk_column(i, t, threads));
     } else {
       load_chunk<T, false>(z, p.K, i, t, threads, 0.0f, held[i].f);
     }
@@ -125,7 +119,7 @@ __global__ void __launch_bounds__(512) layer_norm_kernel(FwdParams p) {
     held[i].values(v);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (!VEC && row_column<false>(i, j, t, threads) >= p.K) v[j] = mu;
+      if (!VEC && chunk_column(i, t, threads) + j >= p.K) v[j] = mu;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const F2 d = add2(f2(v[2 * j], v[2 * j + 1]), f2(-mu, -mu));
@@ -148,7 +142,7 @@ __global__ void __launch_bounds__(512) layer_norm_kernel(FwdParams p) {
     if (p.ckpt >= 0) {
       uint8_t* codes = p.codes + static_cast<size_t>(m) * p.K;
       uint8_t* scales = p.scales + static_cast<size_t>(m) * ((p.K + kCkptGroup - 1) / kCkptGroup);
-      const uint32_t top = VEC ? held[i].largest() : 0u;
+      const uint32_t top = held[i].largest();
       if (p.ckpt == SVDQ_CKPT8_INT8)
         ckpt_store_chunk<SVDQ_CKPT8_INT8, VEC>(codes, scales, p.K, i, t, threads, top, v);
       else
@@ -218,7 +212,7 @@ __global__ void __launch_bounds__(32 * (kBackwardWarps + 1)) layer_norm_backward
   __shared__ int s_abort;
   constexpr int kFmt = SRC == 2 ? SVDQ_CKPT8_E4M3 : SVDQ_CKPT8_INT8;
   // chunks of a row held across its reduction; with more than two the row is read again (in place: dZ may be
-  // dY, of which the element layout then holds what it overwrites)
+  // dY, and without the ring the row is held whole)
   constexpr int kHeld = NV <= 2 || !VEC ? NV : 1;
   const int threads = p.warps * 32, teams = p.teams, workers = teams * threads;
   const int team = threadIdx.x / threads, t = threadIdx.x % threads, lane = threadIdx.x & 31;
@@ -319,7 +313,7 @@ __global__ void __launch_bounds__(32 * (kBackwardWarps + 1)) layer_norm_backward
   int col[NV], mcol[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c0 = row_column<true>(i, 0, t, threads);
+    const int c0 = chunk_column(i, t, threads);
     col[i] = c0 < p.K ? c0 : 0;
     mcol[i] = c0 < p.K ? c0 : p.K;
   }

@@ -1,18 +1,18 @@
 // Row operands of the layer norm and checkpoint kernels: eight values at a time as fp32, and the
 // 8-bit checkpoint codec.
 //
-// A team of `threads` (a multiple of 32) threads covers a row of K columns in one of two layouts:
-//   vector   thread t owns columns 8 (i threads + t) + j, j < 8: one 16-byte access per 8 values
-//            (two for fp32); K, the row strides and the addresses allow it
-//   element  thread t owns columns (8 i + j) threads + t: any K, stride and alignment, 2- or 4-byte
-//            accesses that are contiguous over a warp
-// A checkpoint group (32 consecutive columns) is 4 neighbouring threads' vectors in the first and
-// one j of a whole warp in the second, so its largest magnitude is a warp shuffle away.
+// A team of `threads` (a multiple of 32) threads covers a row of K columns in chunks of 8: thread t owns
+// columns 8 (i threads + t) + j, j < 8.  Where K, the row strides and the addresses allow it (VEC) a
+// chunk is one 16-byte access (two for fp32); else each row takes the widest accesses that its own
+// address allows (16, 4 or an element's bytes), and the chunk that K cuts takes its elements one by one.
+// A checkpoint group (32 consecutive columns) is 4 neighbouring threads' chunks, so its largest
+// magnitude is two shuffles away.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "svdq.h"
 
@@ -48,6 +48,7 @@ __device__ __forceinline__ void unpack8(const uint4& a, float (&v)[8], const __h
     v[2 * j] = f.x, v[2 * j + 1] = f.y;
   }
 }
+__device__ __forceinline__ void unpack8(const uint4&, float (&)[8], const float*) {}  // no 16-bit words
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
   unpack8(*reinterpret_cast<const uint4*>(p), v, p);
@@ -122,43 +123,68 @@ __device__ __forceinline__ void load8_pairs(const T* p, F2 (&v)[4]) {
   for (int j = 0; j < 4; ++j) v[j] = f2(f[2 * j], f[2 * j + 1]);
 }
 
-// Column of value j of chunk i of thread t.
-template <bool VEC>
-__device__ __forceinline__ int row_column(int i, int j, int t, int threads) {
-  return VEC ? (i * threads + t) * 8 + j : (i * 8 + j) * threads + t;
+// The first column of chunk i of thread t.
+__device__ __forceinline__ int chunk_column(int i, int t, int threads) { return (i * threads + t) * 8; }
+
+// The first n of 8 values at any address that is aligned to its elements; `fill` for the others.
+template <typename T>
+__device__ __forceinline__ void load_any(const T* p, int n, float fill, float (&v)[8]) {
+  const uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+  if (n == 8 && low % 16 == 0) {
+    load8(p, v);
+  } else if (n == 8 && sizeof(T) == 2 && low % 4 == 0) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+    unpack8(make_uint4(w[0], w[1], w[2], w[3]), v, p);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? to_f32(p[j]) : fill;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_any(T* p, int n, const float (&v)[8]) {
+  const uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+  if (n == 8 && low % 16 == 0) {
+    store8(p, v);
+  } else if (n == 8 && sizeof(T) == 2 && low % 4 == 0) {
+    T h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = from_f32<T>(v[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint16_t a, b;
+      memcpy(&a, &h[2 * j], 2);
+      memcpy(&b, &h[2 * j + 1], 2);
+      reinterpret_cast<uint32_t*>(p)[j] = a | static_cast<uint32_t>(b) << 16;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = from_f32<T>(v[j]);
+  }
 }
 
 // Chunk i of a row: columns beyond K give `fill`.
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_chunk(const T* row, int K, int i, int t, int threads, float fill, float (&v)[8]) {
-  if (VEC) {
-    const int c = row_column<true>(i, 0, t, threads);
-    if (c < K) {
+  const int c = chunk_column(i, t, threads);
+  if (c < K) {
+    if (VEC)
       load8(row + c, v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = fill;
-    }
+    else
+      load_any(row + c, min(8, K - c), fill, v);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = row_column<false>(i, j, t, threads);
-      v[j] = c < K ? to_f32(row[c]) : fill;
-    }
+    for (int j = 0; j < 8; ++j) v[j] = fill;
   }
 }
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_chunk(T* row, int K, int i, int t, int threads, const float (&v)[8]) {
-  if (VEC) {
-    const int c = row_column<true>(i, 0, t, threads);
-    if (c < K) store8(row + c, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = row_column<false>(i, j, t, threads);
-      if (c < K) row[c] = from_f32<T>(v[j]);
-    }
-  }
+  const int c = chunk_column(i, t, threads);
+  if (c >= K) return;
+  if (VEC)
+    store8(row + c, v);
+  else
+    store_any(row + c, min(8, K - c), v);
 }
 
 // A vector whose type is known at run time (svdq_dtype).
@@ -308,57 +334,60 @@ struct Raw8<float> {
   }
 };
 
+// A chunk of a row as it was read: packed where the vector layout reads it so.
+template <typename T, bool VEC>
+struct Held : Raw8<T> {};
+template <typename T>
+struct Held<T, false> : Raw8<float> {};
+
+// The codes of a chunk, at any address, and its group's scale byte.
+template <int FMT, bool VEC>
+__device__ __forceinline__ void ckpt_store_codes(uint8_t* codes, uint8_t* scales, int c, int K, uint32_t byte,
+                                                 const float (&v)[8]) {
+  const uint2 q = make_uint2(ckpt_codes4<FMT>(v[0], v[1], v[2], v[3], byte), ckpt_codes4<FMT>(v[4], v[5], v[6], v[7], byte));
+  if (VEC || (c + 8 <= K && reinterpret_cast<uintptr_t>(codes + c) % 8 == 0)) {
+    *reinterpret_cast<uint2*>(codes + c) = q;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < K) codes[c + j] = static_cast<uint8_t>((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+  }
+  if (c % kCkptGroup == 0) scales[c / kCkptGroup] = static_cast<uint8_t>(byte);
+}
+
 // Writes chunk i of a row's checkpoint: codes (K bytes) and scales (ceil(K / 32) bytes).  Every lane
-// of the warp calls it; columns beyond K hold 0 (`top`: the vector layout's largest magnitude).
+// of the warp calls it, with its chunk's largest magnitude; columns beyond K hold 0.
 template <int FMT, bool VEC>
 __device__ __forceinline__ void ckpt_store_chunk(uint8_t* codes, uint8_t* scales, int K, int i, int t, int threads,
                                                  uint32_t top, const float (&v)[8]) {
-  if (VEC) {
-    uint32_t m = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t b = ckpt_scale_byte<FMT>(m);
-    const int c = row_column<true>(i, 0, t, threads);
-    if (c < K) {
-      *reinterpret_cast<uint2*>(codes + c) = make_uint2(ckpt_codes4<FMT>(v[0], v[1], v[2], v[3], b),
-                                                       ckpt_codes4<FMT>(v[4], v[5], v[6], v[7], b));
-      if (c % kCkptGroup == 0) scales[c / kCkptGroup] = static_cast<uint8_t>(b);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t b = ckpt_scale_byte<FMT>(__reduce_max_sync(0xffffffffu, abs_bits(v[j])));
-      const int c = row_column<false>(i, j, t, threads);
-      if (c < K) {
-        codes[c] = static_cast<uint8_t>(ckpt_codes4<FMT>(v[j], 0.0f, 0.0f, 0.0f, b) & 0xFFu);
-        if (c % kCkptGroup == 0) scales[c / kCkptGroup] = static_cast<uint8_t>(b);
-      }
-    }
-  }
+  uint32_t m = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const int c = chunk_column(i, t, threads);
+  if (c < K) ckpt_store_codes<FMT, VEC>(codes, scales, c, K, ckpt_scale_byte<FMT>(m), v);
 }
 
 // Chunk i of a row from its checkpoint; columns beyond K give 0.
 template <int FMT, bool VEC>
 __device__ __forceinline__ void ckpt_load_chunk(const uint8_t* codes, const uint8_t* scales, int K, int i, int t,
                                                 int threads, float (&v)[8]) {
-  if (VEC) {
-    const int c = row_column<true>(i, 0, t, threads);
-    if (c < K) {
-      const uint2 w = *reinterpret_cast<const uint2*>(codes + c);
-      const float s = ckpt_scale(scales[c / kCkptGroup]);
-      ckpt_values4<FMT>(w.x, s, v);
-      ckpt_values4<FMT>(w.y, s, v + 4);
+  const int c = chunk_column(i, t, threads);
+  uint2 w = make_uint2(0, 0);
+  float s = 0.0f;
+  if (c < K) {
+    if (VEC || (c + 8 <= K && reinterpret_cast<uintptr_t>(codes + c) % 8 == 0)) {
+      w = *reinterpret_cast<const uint2*>(codes + c);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+      for (int j = 0; j < 8; ++j)
+        if (c + j < K) (j < 4 ? w.x : w.y) |= static_cast<uint32_t>(codes[c + j]) << (8 * (j & 3));
     }
-  } else {
+    s = ckpt_scale(scales[c / kCkptGroup]);
+  }
+  ckpt_values4<FMT>(w.x, s, v);
+  ckpt_values4<FMT>(w.y, s, v + 4);
+  if (!VEC) {  // 0 times a group's NaN is none of the row's padding
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = row_column<false>(i, j, t, threads);
-      float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (c < K) ckpt_values4<FMT>(codes[c], ckpt_scale(scales[c / kCkptGroup]), q);
-      v[j] = q[0];
-    }
+    for (int j = 0; j < 8; ++j) v[j] = c + j < K ? v[j] : 0.0f;
   }
 }
 
