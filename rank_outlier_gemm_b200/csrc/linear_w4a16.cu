@@ -369,27 +369,36 @@ __device__ __forceinline__ void multiply_step(const W4A16Params& p, int s, int g
 template <bool INT4, int NT>
 __device__ __forceinline__ void multiply_branch(const W4A16Params& p, const float* s_t, int u, int g, int t,
                                                 float (&acc)[2][NT][4]) {
-  for (int r = 0; r < p.r_pad; r += 16) {
-    uint2 l2[4];
+  constexpr int kAhead = 4;  // steps whose loads of L2 are in flight at once
+  for (int r0 = 0; r0 < p.r_pad; r0 += 16 * kAhead) {
+    uint2 l2[kAhead][4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int n = unit_row<INT4>(u, b, g);
-      l2[b] = n < p.N ? __ldg(reinterpret_cast<const uint2*>(p.L2t + static_cast<size_t>(n) * p.r_pad + r) + t)
-                      : make_uint2(0, 0);
-    }
+    for (int i = 0; i < kAhead; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int m = (j * 8 + g) >> 1;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (m < p.M) v = *reinterpret_cast<const float4*>(s_t + m * p.r_pad + r + 4 * t);
-      uint32_t b0 = bf16x2(v.x, v.y), b1 = bf16x2(v.z, v.w);
-      if (g & 1) {
-        b0 = bf16x2(rest(v.x, pair_lo(b0)), rest(v.y, pair_hi(b0)));
-        b1 = bf16x2(rest(v.z, pair_lo(b1)), rest(v.w, pair_hi(b1)));
+      for (int b = 0; b < 4; ++b) {
+        const int n = unit_row<INT4>(u, b, g), r = r0 + 16 * i;
+        l2[i][b] = n < p.N && r < p.r_pad
+                       ? __ldg(reinterpret_cast<const uint2*>(p.L2t + static_cast<size_t>(n) * p.r_pad + r) + t)
+                       : make_uint2(0, 0);
       }
 #pragma unroll
-      for (int tile = 0; tile < 2; ++tile)
-        mma_bf16(acc[tile][j], l2[2 * tile].x, l2[2 * tile + 1].x, l2[2 * tile].y, l2[2 * tile + 1].y, b0, b1);
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = r0 + 16 * i;
+      if (r >= p.r_pad) break;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int m = (j * 8 + g) >> 1;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (m < p.M) v = *reinterpret_cast<const float4*>(s_t + m * p.r_pad + r + 4 * t);
+        uint32_t b0 = bf16x2(v.x, v.y), b1 = bf16x2(v.z, v.w);
+        if (g & 1) {
+          b0 = bf16x2(rest(v.x, pair_lo(b0)), rest(v.y, pair_hi(b0)));
+          b1 = bf16x2(rest(v.z, pair_lo(b1)), rest(v.w, pair_hi(b1)));
+        }
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile)
+          mma_bf16(acc[tile][j], l2[i][2 * tile].x, l2[i][2 * tile + 1].x, l2[i][2 * tile].y, l2[i][2 * tile + 1].y, b0, b1);
+      }
     }
   }
 }
@@ -435,17 +444,28 @@ __global__ void __launch_bounds__(32 * kWarps, NT > 2 ? 2 : 3) w4a16_kernel(W4A1
   grid_dep_wait();
   const bool branch = p.r_pad > 0 && rank == p.cluster - 1;  // has the last group of steps, which is the shortest
   if (branch) {
-    for (int i = threadIdx.x; i < p.M * p.r_pad; i += blockDim.x) {
-      float v = 0.0f;
-      for (int k = 0; k < p.t_splits; k += 12) {  // all loads of K <= 12288 at once
-        float a[12];
+    const int n = p.M * p.r_pad;
+    for (int i0 = threadIdx.x; i0 < n; i0 += 2 * blockDim.x) {
+      float v[2] = {0.0f, 0.0f};
+      for (int k = 0; k < p.t_splits; k += 6) {  // all loads of K <= 12288 at once, for two values
+        float a[2][6];
 #pragma unroll
-        for (int j = 0; j < 12; ++j)
-          a[j] = k + j < p.t_splits ? p.T[static_cast<size_t>(k + j) * p.M * p.r_pad + i] : 0.0f;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < 12; ++j) v += a[j];
+          for (int j = 0; j < 6; ++j) {
+            const int i = i0 + h * blockDim.x;
+            a[h][j] = k + j < p.t_splits && i < n ? p.T[static_cast<size_t>(k + j) * n + i] : 0.0f;
+          }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 6; ++j) v[h] += a[h][j];
       }
-      s_t[i] = v * __frcp_rn(p.pow2[i / p.r_pad]);  // exact: a power of two
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = i0 + h * blockDim.x;
+        if (i < n) s_t[i] = v[h] * __frcp_rn(p.pow2[i / p.r_pad]);  // exact: a power of two
+      }
     }
     __syncthreads();
   }

@@ -310,35 +310,31 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(WgradParams p) {
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   grid_dep_launch_dependents();
 
-  // the row warps' sums, up to 32 columns of S at a time: [row warps][columns of X][kPitch]; the pitch
-  // spreads a warp's stores over the banks
-  constexpr int kJ = NT < 4 ? NT : 4, kPitch = kJ * 8 + 2;
+  // the row warps' sums: [row warps][columns of X][kPitch]; the pitch spreads a warp's stores over the banks
+  constexpr int kPitch = NT * 8 + 2;
   const int cols = p.col_warps * kTileCols;
   float* sums = reinterpret_cast<float*>(smem);
   float* out = p.out + static_cast<size_t>(blockIdx.y) * p.K * p.r;
+  __syncthreads();
 #pragma unroll
-  for (int j0 = 0; j0 < NT; j0 += kJ) {
-    __syncthreads();
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int j = 0; j < kJ; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int col = cw * kTileCols + (i >> 1) * 32 + 4 * g + 2 * (i & 1) + h;
-          *reinterpret_cast<float2*>(sums + (rw * cols + col) * kPitch + j * 8 + 2 * t) =
-              make_float2(acc[i][j0 + j][2 * h], acc[i][j0 + j][2 * h + 1]);
-        }
-    __syncthreads();
-    for (int i = threadIdx.x; i < cols * kJ * 8; i += kThreads) {
-      const int col = i / (kJ * 8), n = i % (kJ * 8);
-      const float* s = sums + col * kPitch + n;
-      float v = s[0];
+      for (int h = 0; h < 2; ++h) {
+        const int col = cw * kTileCols + (i >> 1) * 32 + 4 * g + 2 * (i & 1) + h;
+        *reinterpret_cast<float2*>(sums + (rw * cols + col) * kPitch + j * 8 + 2 * t) =
+            make_float2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
+      }
+  __syncthreads();
+  for (int i = threadIdx.x; i < cols * NT * 8; i += kThreads) {
+    const int col = i / (NT * 8), n = i % (NT * 8);
+    const float* s = sums + col * kPitch + n;
+    float v = s[0];
 #pragma unroll 4
-      for (int w = 1; w < row_warps; ++w) v += s[w * cols * kPitch];
-      const int k = blockIdx.x * cols + col, c = n0 + j0 * 8 + n;
-      if (k < p.K && c < p.r) out[static_cast<size_t>(k) * p.r + c] = v;
-    }
+    for (int w = 1; w < row_warps; ++w) v += s[w * cols * kPitch];
+    const int k = blockIdx.x * cols + col;
+    if (k < p.K && n0 + n < p.r) out[static_cast<size_t>(k) * p.r + n0 + n] = v;
   }
 }
 
@@ -368,7 +364,7 @@ struct Plan {
 Plan plan(int M, int K, int r, int tile_rows) {
   Plan q{};
   const int tiles = (r + 7) / 8;
-  q.nt = tiles <= 1 ? 1 : tiles <= 2 ? 2 : tiles <= 4 ? 4 : 8;
+  q.nt = tiles <= 1 ? 1 : tiles <= 2 ? 2 : 4;  // 8 would spill: at r = 64 102 us against 56 for two passes (4608 x 12288, int8)
   q.zs = (tiles + q.nt - 1) / q.nt;
   q.col_warps = K >= 17 * 256 + 1 ? 4 : K >= 17 * 128 + 1 ? 2 : 1;
   q.blocks = (K + q.col_warps * kTileCols - 1) / (q.col_warps * kTileCols);
@@ -383,9 +379,8 @@ Plan plan(int M, int K, int r, int tile_rows) {
 
 template <int SRC, int NT>
 svdq_status launch(const WgradParams& p, const Plan& q, cudaStream_t stream) {
-  constexpr int kJ = NT < 4 ? NT : 4;
   const size_t loop = kSBytes + static_cast<size_t>(kWarps) * Tile<SRC>::stages * Tile<SRC>::bytes;
-  const size_t join = static_cast<size_t>(kWarps) * kTileCols * (kJ * 8 + 2) * sizeof(float);
+  const size_t join = static_cast<size_t>(kWarps) * kTileCols * (NT * 8 + 2) * sizeof(float);
   const size_t smem = std::max(loop, join);
   static std::atomic<uint64_t> allowed{0};
   SVDQ_TRY(allow_dynamic_smem(reinterpret_cast<const void*>(wgrad_kernel<SRC, NT>), static_cast<int>(smem), allowed));
@@ -399,8 +394,7 @@ svdq_status launch_nt(const WgradParams& p, const Plan& q, cudaStream_t stream) 
   switch (q.nt) {
     case 1: return launch<SRC, 1>(p, q, stream);
     case 2: return launch<SRC, 2>(p, q, stream);
-    case 4: return launch<SRC, 4>(p, q, stream);
-    default: return launch<SRC, 8>(p, q, stream);
+    default: return launch<SRC, 4>(p, q, stream);
   }
 }
 
