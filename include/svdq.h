@@ -376,9 +376,11 @@ size_t svdq_linear_w4a16_workspace_bytes(const svdq_weights* w, int M); /* 0 out
  * norm; the tokens of one image: adaLN):
  *   y = (z - mu) * rstd * m + shift,  m = scale, or 1 + scale with plus_one.
  * Row m belongs to group m / group_rows; the last group may be shorter.
- * Strides are in elements; 0 means K (rows packed).  Addresses need the
- * alignment of their elements only; K and strides that are multiples of 8 with
- * 16-byte aligned addresses are read in whole 16-byte pieces and run faster.
+ * Strides are in elements; 0 means K (rows packed).  Z, Y, dY, dZ, scale, shift,
+ * dscale and dshift need the alignment of their elements only (stats, codes and
+ * workspace 16 bytes, a checkpoint's scales none); K and strides that are
+ * multiples of 8 (16 where a checkpoint is read) with 16-byte aligned addresses
+ * are read in whole pieces and run faster.
  */
 typedef struct {
   int M, K;           /* rows and channels; K <= 16384, M <= 2^30 */
@@ -415,7 +417,9 @@ svdq_status svdq_layer_norm(const svdq_norm_desc* desc, const void* Z, const voi
  *   workspace  device memory of at least svdq_layer_norm_backward_workspace_bytes
  *           bytes (NULL if that is 0); calls that may run at the same time need
  *           one each
- * The column sums are joined in a fixed order: equal calls give equal bits.
+ * The column sums are joined in a fixed order: equal calls give equal bits.  A
+ * wait that runs out is recorded in the device error word; the outputs of that
+ * call are then unspecified.
  */
 svdq_status svdq_layer_norm_backward(const svdq_norm_desc* desc, const void* dY, const void* Z, const void* codes,
                                      const void* scales, int ckpt_format, const float* stats, const void* scale,

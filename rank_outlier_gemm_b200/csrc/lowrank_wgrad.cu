@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(WgradParams p) {
     __syncthreads();
 
     for (int step = 0; step < n_steps; ++step) {
-      fetch(stage ? stage - 1 : kStages - 1);  // the stage read last
+      __syncwarp();
+      fetch(stage ? stage - 1 : kStages - 1);  // the stage that every lane read last
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       __syncwarp();
       const uint32_t tile = ring + stage * Tile<SRC>::bytes;
