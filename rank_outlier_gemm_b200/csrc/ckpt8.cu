@@ -27,30 +27,40 @@ __device__ __forceinline__ void split_index(uint64_t idx, uint64_t total, uint32
   }
 }
 
+// How rows are addressed: packed rows of whole groups are one long row (the index arithmetic of the others
+// took a fifth of the time: 33.3 against 27.4 us at 4608 x 12288, bf16 to int8).
+enum Layout { kPacked, kVector, kAny };
+
 // kUnroll chunks of 8 values per thread, a group is 4 neighbouring threads' chunks; the chunks' loads are all
 // in flight before the first is used.
 constexpr int kUnroll = 4;
-template <typename T, int FMT, bool VEC>
+template <typename T, int FMT, Layout L>
 __global__ void __launch_bounds__(kThreads) ckpt_encode_kernel(const T* __restrict__ X, int64_t ld, uint64_t total,
                                                             uint32_t per_row, int K, uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales) {
   const int groups = (K + kCkptGroup - 1) / kCkptGroup;
-  Held<T, VEC> held[kUnroll];
-  uint64_t row[kUnroll];
+  Held<T, L != kAny> held[kUnroll];
+  uint64_t row[kUnroll];  // packed: the chunk's first value instead
   uint32_t at[kUnroll];
   bool in[kUnroll];
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
     const uint64_t idx = (static_cast<uint64_t>(blockIdx.x) * kUnroll + i) * kThreads + threadIdx.x;
+    held[i].clear();
+    if constexpr (L == kPacked) {
+      in[i] = idx < total;
+      row[i] = idx * 8;
+      if (in[i]) held[i].load(X + row[i]);
+      continue;
+    }
     split_index(idx < total ? idx : total - 1, total, per_row, row[i], at[i]);
     at[i] *= 8;  // column
     in[i] = idx < total && at[i] < static_cast<uint32_t>(K);
-    held[i].clear();
     if (in[i]) {
       const T* x = X + row[i] * ld + at[i];
-      if constexpr (VEC)
+      if constexpr (L == kVector)
         held[i].load(x);
-      else
+      else if constexpr (L == kAny)
         load_any(x, min(8, K - static_cast<int>(at[i])), 0.0f, held[i].f);
     }
   }
@@ -62,25 +72,37 @@ __global__ void __launch_bounds__(kThreads) ckpt_encode_kernel(const T* __restri
     if (in[i]) {
       float v[8];
       held[i].values(v);
-      ckpt_store_codes<FMT, VEC>(codes + row[i] * K, scales + row[i] * groups, static_cast<int>(at[i]), K,
-                                 ckpt_scale_byte<FMT>(m), v);
+      const uint32_t byte = ckpt_scale_byte<FMT>(m);
+      if constexpr (L == kPacked)  // the places of a row of one group
+        ckpt_store_codes<FMT, true>(codes + row[i] / kCkptGroup * kCkptGroup, scales + row[i] / kCkptGroup,
+                                    static_cast<int>(row[i] % kCkptGroup), kCkptGroup, byte, v);
+      else
+        ckpt_store_codes<FMT, L == kVector>(codes + row[i] * K, scales + row[i] * groups, static_cast<int>(at[i]), K,
+                                            byte, v);
     }
   }
 }
 
-template <typename T, int FMT, bool VEC>
+template <typename T, int FMT, Layout L>
 __global__ void __launch_bounds__(kThreads) ckpt_decode_kernel(const uint8_t* __restrict__ codes,
                                                             const uint8_t* __restrict__ scales, uint64_t total,
                                                             uint32_t per_row, int K, T* __restrict__ X, int64_t ld) {
   const uint64_t idx = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x;
   if (idx >= total) return;
+  float v[8];
+  if (L == kPacked) {
+    const uint64_t group = idx / 4;
+    const int at = static_cast<int>(idx % 4);
+    ckpt_load_chunk<FMT, true>(codes + group * kCkptGroup, scales + group, kCkptGroup, 0, at, 0, v);
+    store8(X + idx * 8, v);
+    return;
+  }
   uint64_t row = 0;
   uint32_t at = 0;
   split_index(idx, total, per_row, row, at);
-  float v[8];
-  ckpt_load_chunk<FMT, VEC>(codes + row * K, scales + row * ((K + kCkptGroup - 1) / kCkptGroup), K, 0,
-                            static_cast<int>(at), 0, v);
-  store_chunk<T, VEC>(X + row * ld, K, 0, static_cast<int>(at), 0, v);
+  ckpt_load_chunk<FMT, L == kVector>(codes + row * K, scales + row * ((K + kCkptGroup - 1) / kCkptGroup), K, 0,
+                                     static_cast<int>(at), 0, v);
+  store_chunk<T, L == kVector>(X + row * ld, K, 0, static_cast<int>(at), 0, v);
 }
 
 struct Grid {
@@ -99,15 +121,26 @@ svdq_status item_grid(int M, int items, int pad, int per_thread, Grid* g) {
   return SVDQ_OK;
 }
 
+Layout layout(const void* X, int K, int64_t ld) {
+  if (K % 8 || ld % 8 || !aligned16(X)) return kAny;
+  return K % kCkptGroup == 0 && ld == K ? kPacked : kVector;
+}
+
 template <typename T, int FMT>
 svdq_status encode(const void* X, int64_t ld, int M, int K, uint8_t* codes, uint8_t* scales, cudaStream_t stream) {
   Grid g;
   const T* x = static_cast<const T*>(X);
   SVDQ_TRY(item_grid(M, (K + 7) / 8, 4, kUnroll, &g));
-  if (K % 8 == 0 && ld % 8 == 0 && aligned16(X))
-    ckpt_encode_kernel<T, FMT, true><<<g.blocks, kThreads, 0, stream>>>(x, ld, g.total, g.per_row, K, codes, scales);
-  else
-    ckpt_encode_kernel<T, FMT, false><<<g.blocks, kThreads, 0, stream>>>(x, ld, g.total, g.per_row, K, codes, scales);
+  switch (layout(X, K, ld)) {
+    case kPacked:
+      ckpt_encode_kernel<T, FMT, kPacked><<<g.blocks, kThreads, 0, stream>>>(x, ld, g.total, g.per_row, K, codes, scales);
+      break;
+    case kVector:
+      ckpt_encode_kernel<T, FMT, kVector><<<g.blocks, kThreads, 0, stream>>>(x, ld, g.total, g.per_row, K, codes, scales);
+      break;
+    default:
+      ckpt_encode_kernel<T, FMT, kAny><<<g.blocks, kThreads, 0, stream>>>(x, ld, g.total, g.per_row, K, codes, scales);
+  }
   SVDQ_CUDA_TRY(cudaGetLastError());
   return SVDQ_OK;
 }
@@ -117,10 +150,16 @@ svdq_status decode(const uint8_t* codes, const uint8_t* scales, int M, int K, vo
   Grid g;
   T* x = static_cast<T*>(X);
   SVDQ_TRY(item_grid(M, (K + 7) / 8, 1, 1, &g));
-  if (K % 8 == 0 && ld % 8 == 0 && aligned16(X))
-    ckpt_decode_kernel<T, FMT, true><<<g.blocks, kThreads, 0, stream>>>(codes, scales, g.total, g.per_row, K, x, ld);
-  else
-    ckpt_decode_kernel<T, FMT, false><<<g.blocks, kThreads, 0, stream>>>(codes, scales, g.total, g.per_row, K, x, ld);
+  switch (layout(X, K, ld)) {
+    case kPacked:
+      ckpt_decode_kernel<T, FMT, kPacked><<<g.blocks, kThreads, 0, stream>>>(codes, scales, g.total, g.per_row, K, x, ld);
+      break;
+    case kVector:
+      ckpt_decode_kernel<T, FMT, kVector><<<g.blocks, kThreads, 0, stream>>>(codes, scales, g.total, g.per_row, K, x, ld);
+      break;
+    default:
+      ckpt_decode_kernel<T, FMT, kAny><<<g.blocks, kThreads, 0, stream>>>(codes, scales, g.total, g.per_row, K, x, ld);
+  }
   SVDQ_CUDA_TRY(cudaGetLastError());
   return SVDQ_OK;
 }
