@@ -81,7 +81,7 @@ __device__ __forceinline__ void param_chunk(const void* p, int dtype, size_t off
 }
 
 template <typename T, typename P, int NV, bool VEC>
-__global__ void __launch_bounds__(512) layer_norm_kernel(FwdParams p) {
+__global__ void __launch_bounds__(512, VEC && sizeof(T) == 2 ? 2 : 0) layer_norm_kernel(FwdParams p) {
   __shared__ float red[kForwardWarps][64];
   const int threads = p.warps * 32, team = threadIdx.x / threads, t = threadIdx.x % threads;
   const int m = blockIdx.x * (blockDim.x / threads) + team;
@@ -136,6 +136,8 @@ __global__ void __launch_bounds__(512) layer_norm_kernel(FwdParams p) {
   for (int i = 0; i < NV; ++i) {
     float v[8], a[8], c[8];
     held[i].values(v);
+    // one chunk's parameters at a time: all at once would take the registers of half the warps
+    if (VEC && sizeof(T) == 2) asm volatile("" ::: "memory");
     const bool in = inside(i);
     if (p.scale && in) param_chunk<P, VEC>(p.scale, p.param_dtype, group, p.K, i, t, threads, a);
     if (p.shift && in) param_chunk<P, VEC>(p.shift, p.param_dtype, group, p.K, i, t, threads, c);
@@ -503,9 +505,11 @@ struct Shape {
   int nv, warps, teams;
 };
 
-// Forward: up to 5 chunks of 8 values a thread; one warp a row while that reaches (no barriers), else
-// the chunk count that wastes the fewest threads, the larger one when they tie.
-Shape forward_shape(int K) {
+// Forward: one warp a row while 5 chunks of 8 values a thread reach (no barriers), else the chunk count that
+// wastes the fewest threads; when they tie the smaller one for 16-bit rows (more warps: 4608 x 12288 bf16
+// 108 -> 72 us) and the larger one for fp32 (8192 x 4096: 53 against 65 us).  A ring of rows as the backward
+// has it was slower (8192 x 4096 bf16 63 against 46 us).
+Shape forward_shape(int K, bool narrow) {
   const int nvec = (K + 7) / 8;
   Shape s{};
   if (nvec <= 160) {
@@ -513,8 +517,8 @@ Shape forward_shape(int K) {
     s.nv = (nvec + 31) / 32;
   } else {
     int best = 1 << 30;
-    for (int nv = 4; nv >= 2; --nv) {
-      const int warps = (nvec + 32 * nv - 1) / (32 * nv);
+    for (int i = 0; i < 3; ++i) {
+      const int nv = narrow ? 2 + i : 4 - i, warps = (nvec + 32 * nv - 1) / (32 * nv);
       if (warps <= 16 && warps * nv < best) best = warps * nv, s.nv = nv, s.warps = warps;
     }
   }
@@ -524,18 +528,19 @@ Shape forward_shape(int K) {
 
 // Backward: 16 sums a chunk stay in registers over all rows and 16 more values across a row's reduction:
 // two chunks a thread while 16 warps reach, then three or four.
-Shape backward_shape(int K) {
+Shape backward_shape(int K, int rows) {
   const int nvec = (K + 7) / 8;
   Shape s{};
   s.nv = nvec <= 32 ? 1 : nvec <= 1024 ? 2 : nvec <= 1536 ? 3 : 4;
   s.warps = (nvec + 32 * s.nv - 1) / (32 * s.nv);
   s.teams = s.warps >= kBackwardWarps ? 1 : kBackwardWarps / s.warps;
+  if (s.teams > rows) s.teams = rows;  // smaller CTAs, more of them per SM, for groups of a few rows
   return s;
 }
 
 // CTAs that share a group's rows: one per SM over all groups, four rows a team at least.
 int backward_splits(int K, int rows, int groups) {
-  const Shape s = backward_shape(K);
+  const Shape s = backward_shape(K, rows);
   const int want = (kMaxSplits + groups - 1) / groups;  // at most kMaxSplits
   const int most = (rows + 4 * s.teams - 1) / (4 * s.teams);
   return want < most ? want : most;
@@ -634,7 +639,7 @@ svdq_status launch_layer_norm(const NormArgs& a, const void* Z, const void* scal
                               float* stats, uint8_t* codes, uint8_t* scales, int ckpt, cudaStream_t stream) {
   FwdParams p{Z, scale, shift, Y, reinterpret_cast<float2*>(stats), codes, scales, a.ld_z, a.ld_y, a.ld_param,
               a.M, a.K, a.rows, a.param_dtype, 0, codes ? ckpt : -1, a.eps, a.plus_one ? 1.0f : 0.0f};
-  const Shape s = forward_shape(a.K);
+  const Shape s = forward_shape(a.K, a.dtype != SVDQ_DTYPE_FP32);
   p.warps = s.warps;
   const bool vec = vector_rows(a.K, {Z, scale, shift, Y, codes}, {a.ld_z, a.ld_y, a.ld_param});
   switch (a.dtype) {
@@ -648,7 +653,7 @@ svdq_status launch_layer_norm_backward(const NormArgs& a, const void* dY, const 
                                        const uint8_t* scales, int ckpt, const float* stats, const void* scale,
                                        void* dZ, float* dscale, float* dshift, void* workspace, cudaStream_t stream) {
   const int groups = (a.M + a.rows - 1) / a.rows;
-  const Shape s = backward_shape(a.K);
+  const Shape s = backward_shape(a.K, a.rows);
   BwdParams p{dY, Z, codes, scales, reinterpret_cast<const float2*>(stats), scale, dZ, dscale, dshift, nullptr,
               a.ld_z, a.ld_dy, a.ld_dz, a.ld_param, a.M, a.K, a.rows, backward_splits(a.K, a.rows, groups),
               a.param_dtype, s.warps, s.teams, 0, 0, a.plus_one ? 1.0f : 0.0f, nullptr, 0};
