@@ -10,6 +10,12 @@
 // fp32.  In the backward a thread keeps its columns over all rows that its CTA takes, so the column
 // sums stay in registers too; CTAs that share a group leave partial sums in the workspace and a
 // second kernel adds them in a fixed order (no atomics: equal calls give equal bits).
+//
+// Measured (one B200, device time in a graph; the copy rate would take the time in brackets): forward
+// bf16 8192 x 4096 43 us (20.5), fp32 53 (40.9), bf16 4096 x 1152 with an int8 checkpoint 10.2 (3.6); gradient
+// bf16 8192 x 4096 38 (30.7), 4500 x 4096 from an int8 checkpoint 26.2 (14.2), 8192 x 640 12.9 (4.8).  The
+// 16-bit forward and decoding issue for half of their time, and the rest is a row's chain of two reductions
+// with 32 warps per SM to cover it.
 #include <algorithm>
 #include <initializer_list>
 #include <type_traits>
@@ -26,6 +32,7 @@ using namespace dev;
 // Warps of a CTA, shared out to teams (a team may have more: it is alone then).  The backward takes one CTA
 // of 16 warps per SM, which halves the partial sums that two of 8 would leave.
 constexpr int kForwardWarps = 8, kBackwardWarps = 16;
+constexpr int kSMs = 148;
 
 // Sums over a team of `warps` warps, the same in every thread.  `red` holds two buffers of 2 x 16
 // values per team, used in turn: the barrier of one call separates the reads of the call before from
@@ -67,6 +74,7 @@ struct FwdParams {
   uint8_t* scales;
   int64_t ld_z, ld_y, ld_param;
   int M, K, rows, param_dtype, warps, ckpt;  // ckpt: -1 none, else svdq_ckpt8_format
+  int ahead;                                 // rows ahead that are brought into L2, 0: none
   float eps, one;
 };
 
@@ -88,6 +96,7 @@ __global__ void __launch_bounds__(512, VEC && sizeof(T) == 2 ? 2 : 0) layer_norm
   if (m >= p.M) return;  // whole teams: a barrier has all of its team's warps
   int turn = 0;
   const T* z = static_cast<const T*>(p.Z) + m * p.ld_z;
+  if (VEC && p.ahead && t == 0 && m + p.ahead < p.M) bulk_prefetch(z + p.ahead * p.ld_z, p.K * sizeof(T));
   Held<T, VEC> held[NV];
   auto inside = [&](int i) { return chunk_column(i, t, threads) < p.K; };
 #pragma unroll
@@ -470,7 +479,6 @@ __global__ void __launch_bounds__(32 * (kBackwardWarps + 1)) layer_norm_backward
 
 // dscale and dshift from the partial sums: 32 columns per CTA, its warps share the splits out.
 // Launched while the first kernel still runs; the wait is for its results.
-constexpr int kMaxSplits = 148;  // one CTA per SM
 __global__ void __launch_bounds__(1024) layer_norm_sum_kernel(const float* __restrict__ partial, int splits, int K,
                                                            float* dscale, float* dshift) {
   __shared__ float part[32][33];
@@ -507,7 +515,7 @@ struct Shape {
 
 // Forward: one warp a row while 5 chunks of 8 values a thread reach (no barriers), else the chunk count that
 // wastes the fewest threads; when they tie the smaller one for 16-bit rows (more warps: 4608 x 12288 bf16
-// 108 -> 72 us) and the larger one for fp32 (8192 x 4096: 53 against 65 us).  A ring of rows as the backward
+// 108 -> 72 us then) and the larger one for fp32 (8192 x 4096: 53 against 65 us).  A ring of rows as the backward
 // has it was slower (8192 x 4096 bf16 63 against 46 us).
 Shape forward_shape(int K, bool narrow) {
   const int nvec = (K + 7) / 8;
@@ -541,7 +549,7 @@ Shape backward_shape(int K, int rows) {
 // CTAs that share a group's rows: one per SM over all groups, four rows a team at least.
 int backward_splits(int K, int rows, int groups) {
   const Shape s = backward_shape(K, rows);
-  const int want = (kMaxSplits + groups - 1) / groups;  // at most kMaxSplits
+  const int want = (kSMs + groups - 1) / groups;
   const int most = (rows + 4 * s.teams - 1) / (4 * s.teams);
   return want < most ? want : most;
 }
@@ -638,9 +646,12 @@ size_t layer_norm_backward_workspace(int M, int K, int rows) {
 svdq_status launch_layer_norm(const NormArgs& a, const void* Z, const void* scale, const void* shift, void* Y,
                               float* stats, uint8_t* codes, uint8_t* scales, int ckpt, cudaStream_t stream) {
   FwdParams p{Z, scale, shift, Y, reinterpret_cast<float2*>(stats), codes, scales, a.ld_z, a.ld_y, a.ld_param,
-              a.M, a.K, a.rows, a.param_dtype, 0, codes ? ckpt : -1, a.eps, a.plus_one ? 1.0f : 0.0f};
+              a.M, a.K, a.rows, a.param_dtype, 0, codes ? ckpt : -1, 0, a.eps, a.plus_one ? 1.0f : 0.0f};
   const Shape s = forward_shape(a.K, a.dtype != SVDQ_DTYPE_FP32);
   p.warps = s.warps;
+  // 8 warps' rows per SM ahead, a quarter of those at work: 4608 x 12288 bf16 71.5 -> 67 us, 8192 x 4096 46 -> 43
+  // (half and all of them the same, twice as many slower); no gain for a row per warp or in fp32.
+  if (s.warps > 1 && a.dtype != SVDQ_DTYPE_FP32) p.ahead = (kSMs * 8 + s.warps - 1) / s.warps;
   const bool vec = vector_rows(a.K, {Z, scale, shift, Y, codes}, {a.ld_z, a.ld_y, a.ld_param});
   switch (a.dtype) {
     case SVDQ_DTYPE_BF16: return forward_type<__nv_bfloat16>(p, s, vec, a.dtype, stream);

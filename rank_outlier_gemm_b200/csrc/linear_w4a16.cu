@@ -15,6 +15,12 @@
 // not rounded further than fp32 sums are.  The first kernel lays these columns out in the order the
 // second one's MMA fragments read them and computes T (bf16 inputs, exact products, fp32 sums).
 //
+// Measured (one B200, device time in a graph): NVFP4 1 x 4096 -> 24576, rank 32: 17.6 us, 3.3 TB/s, half
+// the copy rate.  Reading alone takes 14.3 us of it, the products alone 13.7, and 4.8 are in both (two
+// launches, the first kernel, the join): registers for three CTAs per SM leave the two to overlap only in
+// part.  Smaller layers are that fixed part: INT4 5 x 1280 -> 10240 10.8 us, NVFP4 16 x 10240 -> 1280 12.4,
+// 1 x 640 -> 640 5.4.
+//
 // Order of k.  A contraction may run in any order, so a thread takes 16 consecutive bytes (32
 // weights) of a row and feeds them to 8 MMA steps; the columns of X are laid out to match.
 #include <cuda_bf16.h>

@@ -11,6 +11,10 @@
 // fragments of S (exact), which costs 2 products per 16 rows and 8 columns of S instead of one per
 // value of X; a warp's 64 columns are two scale groups and each MMA stays in one.
 //
+// Measured (one B200, device time in a graph): int8 4608 x 12288, r = 32: 29.7 us against 9.2 for one pass
+// over the bytes.  About 8 us are fixed (first copies, joins, second kernel), 13 the decoding and products
+// alone; the scale bytes, a sector each per row and 64 columns, cost 5.  bf16 4099 x 1152, r = 16: 6.9 us.
+//
 // A CTA holds its rows of S in shared memory; each warp copies its 16 x 64 tiles of X ahead through a
 // ring of its own, so the main loop has no CTA barrier.  Sums are joined by ordinary fp32 additions in
 // a fixed order: the CTA's row warps in shared memory, then the CTAs that share the rows by a second kernel

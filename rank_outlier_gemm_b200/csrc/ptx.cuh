@@ -127,6 +127,11 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+// Brings 16-byte aligned memory, a multiple of 16 bytes, into L2.
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // 8- and 4-byte asynchronous copies global -> shared, and the arrival of this thread's earlier ones on
 // an mbarrier whose count includes it.
 __device__ __forceinline__ void copy8_async(void* dst, const void* src) {

@@ -36,6 +36,19 @@ def test_rows_far_apart():
     assert torch.equal(Z.double().cpu(), torch.from_numpy(ref_decode(ck[0].cpu().numpy(), ck[1].cpu().numpy(), "int8")))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_more_rows_than_are_at_work(dt):
+    """The forward asks for rows ahead of the ones at work: of a view with gaps, in place, to the last row."""
+    M, K, gr = 1301, 2056, 100
+    Z = rows(6, M, K, DT[dt], 1.0, K + 24)
+    before = Z.clone()
+    scale, shift = params(7, M, K, gr, "fp32", True)
+    L = lib()
+    stats = torch.empty((M, 2), device="cuda")
+    L.svdq_layer_norm(Z, scale, shift, Z, stats, 1e-6, group_rows=gr, plus_one=True)
+    check_forward(before, Z, stats, of_group(f64(scale), M, gr) + 1, of_group(f64(shift), M, gr), 1e-6, DT[dt])
+
+
 def test_a_checkpoint_of_more_than_2_to_31_values():
     M, K = 70000, 31008
     L = lib()
