@@ -479,8 +479,8 @@ __global__ void __launch_bounds__(32 * (kBackwardWarps + 1)) layer_norm_backward
 
 // dscale and dshift from the partial sums: 32 columns per CTA, its warps share the splits out.
 // Launched while the first kernel still runs; the wait is for its results.
-__global__ void __launch_bounds__(1024) layer_norm_sum_kernel(const float* __restrict__ partial, int splits, int K,
-                                                           float* dscale, float* dshift) {
+__global__ void __launch_bounds__(1024) layer_norm_sum_kernel(const float* partial, int splits, int K, float* dscale,
+                                                           float* dshift) {
   __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int c = blockIdx.x * 32 + lane, group = blockIdx.y, which = blockIdx.z;
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(1024) layer_norm_sum_kernel(const float* __res
     for (int i = warp; i < splits; i += 5 * warps) {  // five loads in flight
       float v[5];
 #pragma unroll
-      for (int j = 0; j < 5; ++j) v[j] = i + j * warps < splits ? __ldg(from + (i + j * warps) * pitch) : 0.0f;
+      for (int j = 0; j < 5; ++j) v[j] = i + j * warps < splits ? ld_after_wait(from + (i + j * warps) * pitch) : 0.0f;
 #pragma unroll
       for (int j = 0; j < 5; ++j) s += v[j];
     }

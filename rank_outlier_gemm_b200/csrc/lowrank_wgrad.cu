@@ -343,8 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(WgradParams p) {
   }
 }
 
-__global__ void __launch_bounds__(256) wgrad_sum_kernel(const float* __restrict__ partial, int parts, size_t n,
-                                                     float* __restrict__ G) {
+__global__ void __launch_bounds__(256) wgrad_sum_kernel(const float* partial, int parts, size_t n, float* G) {
   const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
   grid_dep_wait();
   if (i >= n) return;
@@ -352,7 +351,7 @@ __global__ void __launch_bounds__(256) wgrad_sum_kernel(const float* __restrict_
   for (int j = 0; j < parts; j += 8) {  // eight loads in flight
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = j + e < parts ? partial[(j + e) * n + i] : 0.0f;
+    for (int e = 0; e < 8; ++e) v[e] = j + e < parts ? ld_after_wait(partial + (j + e) * n + i) : 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) s += v[e];
   }

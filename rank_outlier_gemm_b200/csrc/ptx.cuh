@@ -209,6 +209,16 @@ __device__ __forceinline__ void grid_dep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Reads what the kernel ahead wrote, after grid_dep_wait().  That memory changes while this kernel is
+// already there, so it may not be read as constant data (__ldg, or a const __restrict__ pointer, which
+// lets the compiler use the same load and move it ahead of the wait): an ordinary load that stays behind
+// the wait.
+__device__ __forceinline__ float ld_after_wait(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
