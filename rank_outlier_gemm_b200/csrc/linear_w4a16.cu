@@ -82,10 +82,6 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
 
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 // What rounding to `hi` left of v; nothing of an infinity or a NaN, which stays in hi alone.
 __device__ __forceinline__ float rest(float v, float hi) { return isfinite(hi) ? v - hi : 0.0f; }
 
@@ -371,9 +367,10 @@ __device__ __forceinline__ void multiply_step(const W4A16Params& p, int s, int g
 }
 
 // The low-rank branch as MMA steps of 16 ranks: rows of L2 / alpha_w against the tokens' T over their
-// scale, as bf16 hi + lo columns.
+// scale, `s_t`, in three bf16 parts, which are all 24 bits of the fp32 sum.  Two parts are a token's columns, the
+// third takes a second product.
 template <bool INT4, int NT>
-__device__ __forceinline__ void multiply_branch(const W4A16Params& p, const float* s_t, int u, int g, int t,
+__device__ __forceinline__ void multiply_branch(const W4A16Params& p, const uint16_t* s_t, int u, int g, int t,
                                                 float (&acc)[2][NT][4]) {
   constexpr int kAhead = 4;  // steps whose loads of L2 are in flight at once
   for (int r0 = 0; r0 < p.r_pad; r0 += 16 * kAhead) {
@@ -394,16 +391,18 @@ __device__ __forceinline__ void multiply_branch(const W4A16Params& p, const floa
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int m = (j * 8 + g) >> 1;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (m < p.M) v = *reinterpret_cast<const float4*>(s_t + m * p.r_pad + r + 4 * t);
-        uint32_t b0 = bf16x2(v.x, v.y), b1 = bf16x2(v.z, v.w);
-        if (g & 1) {
-          b0 = bf16x2(rest(v.x, pair_lo(b0)), rest(v.y, pair_hi(b0)));
-          b1 = bf16x2(rest(v.z, pair_lo(b1)), rest(v.w, pair_hi(b1)));
+        const uint16_t* parts = s_t + m * 3 * p.r_pad + r + 4 * t;  // an even column's are 0 and 2, an odd one's is 1
+        uint2 first = make_uint2(0, 0), third = first;
+        if (m < p.M) {
+          first = *reinterpret_cast<const uint2*>(parts + (g & 1) * p.r_pad);
+          if (!(g & 1)) third = *reinterpret_cast<const uint2*>(parts + 2 * p.r_pad);
         }
 #pragma unroll
-        for (int tile = 0; tile < 2; ++tile)
-          mma_bf16(acc[tile][j], l2[i][2 * tile].x, l2[i][2 * tile + 1].x, l2[i][2 * tile].y, l2[i][2 * tile + 1].y, b0, b1);
+        for (int tile = 0; tile < 2; ++tile) {
+          const uint2 even = l2[i][2 * tile], odd = l2[i][2 * tile + 1];
+          mma_bf16(acc[tile][j], even.x, odd.x, even.y, odd.y, first.x, first.y);
+          mma_bf16(acc[tile][j], even.x, odd.x, even.y, odd.y, third.x, third.y);
+        }
       }
     }
   }
@@ -421,6 +420,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT > 2 ? 2 : 3) w4a16_kernel(W4A1
   constexpr int kGroupFloats = NT * 4 * kPitch;
   extern __shared__ __align__(16) uint8_t smem[];  // the warps' rings, the groups' sums
                                                    // [kGroups][NT * 4 tokens][kPitch], T over the tokens' scales
+                                                   // [M][3 parts][r_pad] in bf16
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int slice = warp % kSlices, kg = warp / kSlices;
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT > 2 ? 2 : 3) w4a16_kernel(W4A1
   const int jobs = p.M * kRows;
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStageBytes + lane * 16;
   float* red = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes);
-  float* s_t = red + kGroups * kGroupFloats;
+  uint16_t* s_t = reinterpret_cast<uint16_t*>(red + kGroups * kGroupFloats);
 
   // this warp's steps, unit by unit, as they are fetched
   int next_block = first < p.steps ? static_cast<int>(blockIdx.x) / p.cluster : p.blocks, next_step = first;
@@ -470,7 +470,16 @@ __global__ void __launch_bounds__(32 * kWarps, NT > 2 ? 2 : 3) w4a16_kernel(W4A1
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int i = i0 + h * blockDim.x;
-        if (i < n) s_t[i] = v[h] * __frcp_rn(p.pow2[i / p.r_pad]);  // exact: a power of two
+        if (i >= n) continue;
+        const int m = i / p.r_pad;
+        float left = v[h] * __frcp_rn(p.pow2[m]);  // exact: a power of two
+        uint16_t* to = s_t + 2 * m * p.r_pad + i;
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          const __nv_bfloat16 b = __float2bfloat16_rn(left);
+          to[part * p.r_pad] = __bfloat16_as_ushort(b);
+          left = rest(left, __bfloat162float(b));
+        }
       }
     }
     __syncthreads();
@@ -559,7 +568,7 @@ svdq_status launch_main(W4A16Params& p, cudaStream_t stream) {
   p.blocks = (units + kSlices - 1) / kSlices;
   const size_t smem = static_cast<size_t>(kWarps) * kStages * kStageBytes +
                       static_cast<size_t>(kGroups) * NT * 4 * (kSlices * kUnitRows + 8) * sizeof(float) +
-                      static_cast<size_t>(p.M) * p.r_pad * sizeof(float);
+                      static_cast<size_t>(p.M) * p.r_pad * 3 * sizeof(uint16_t);
   // as many CTAs as the SMs hold at a time, so that the units are dealt out evenly
   const int resident = kSMs * (NT > 2 ? 2 : 3);
   const int grid = p.cluster > 1 || p.blocks < resident ? p.blocks : resident;
