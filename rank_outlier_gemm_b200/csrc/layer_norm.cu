@@ -343,16 +343,16 @@ __global__ void __launch_bounds__(32 * (kBackwardWarps + 1)) layer_norm_backward
       const uint8_t* row_s = here + at.scales + team * scale_row +
                              ((static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.scales)) +
                                static_cast<uint32_t>(block) * static_cast<uint32_t>(scale_row)) & 3);
-      const float rstd = st.y, shift = -st.x * rstd;  // xh = z rstd - mu rstd
+      const float rstd = st.y;
       // chunk i: dy, xh and the multipliers
       auto read = [&](int i, F2(&d)[4], F2(&xh)[4], F2(&w)[4]) {
-        float mult = rstd;
+        float scale = 1.0f;  // of a checkpoint's group
         if (VEC) {
           const int c0 = col[i];
           load8_pairs(row_dy + c0, d);
-          if (SRC) {  // the scale, a power of two, goes into the multiplier
+          if (SRC) {
             ckpt_codes8_pairs<kFmt>(*reinterpret_cast<const uint2*>(row_z + c0), xh);
-            mult *= ckpt_scale(row_s[static_cast<uint32_t>(c0) / kCkptGroup]);
+            scale = ckpt_scale(row_s[static_cast<uint32_t>(c0) / kCkptGroup]);
           } else {
             load8_pairs(reinterpret_cast<const T*>(row_z) + c0, xh);
           }
@@ -361,11 +361,11 @@ __global__ void __launch_bounds__(32 * (kBackwardWarps + 1)) layer_norm_backward
           float a[8], b[8], c[8];
           load_chunk<T, false>(static_cast<const T*>(p.dY) + m * p.ld_dy, p.K, i, t, threads, 0.0f, a);
           if (SRC == 0)
-            load_chunk<T, false>(static_cast<const T*>(p.Z) + m * p.ld_z, p.K, i, t, threads, 0.0f, b);
+            load_chunk<T, false>(static_cast<const T*>(p.Z) + m * p.ld_z, p.K, i, t, threads, st.x, b);
           else
             ckpt_load_chunk<kFmt, false>(p.codes + static_cast<size_t>(m) * p.K,
-                                         p.scales + static_cast<size_t>(m) * scale_row, p.K, i, t, threads, b);
-          load_chunk<float, false>(mul, p.K, i, t, threads, 0.0f, c);  // columns beyond K: g = 0
+                                         p.scales + static_cast<size_t>(m) * scale_row, p.K, i, t, threads, b, st.x);
+          load_chunk<float, false>(mul, p.K, i, t, threads, 0.0f, c);  // columns beyond K: z = mu and g = 0
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             d[j] = f2(a[2 * j], a[2 * j + 1]);
@@ -373,9 +373,11 @@ __global__ void __launch_bounds__(32 * (kBackwardWarps + 1)) layer_norm_backward
             w[j] = f2(c[2 * j], c[2 * j + 1]);
           }
         }
-        const F2 scaled = f2(mult, mult), off = f2(shift, shift);
+        // (z - mu) rstd as the forward has it, not z rstd - mu rstd: that would round at the size of mu rstd.
+        // A checkpoint's code times its scale, a power of two, is exact.
+        const F2 off = f2(-st.x, -st.x), by = f2(scale, scale), rs = f2(rstd, rstd);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) xh[j] = fma2(xh[j], scaled, off);
+        for (int j = 0; j < 4; ++j) xh[j] = mul2(VEC && SRC ? fma2(xh[j], by, off) : add2(xh[j], off), rs);
       };
 #pragma unroll
       for (int i = 0; i < NV; ++i) {

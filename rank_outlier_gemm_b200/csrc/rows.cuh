@@ -345,10 +345,10 @@ __device__ __forceinline__ void ckpt_store_chunk(uint8_t* codes, uint8_t* scales
   if (c < K) ckpt_store_codes<FMT, VEC>(codes, scales, c, K, ckpt_scale_byte<FMT>(m), v);
 }
 
-// Chunk i of a row from its checkpoint; columns beyond K give 0.
+// Chunk i of a row from its checkpoint; columns beyond K give `fill` (a chunk of the vector layout has none).
 template <int FMT, bool VEC>
 __device__ __forceinline__ void ckpt_load_chunk(const uint8_t* codes, const uint8_t* scales, int K, int i, int t,
-                                                int threads, float (&v)[8]) {
+                                                int threads, float (&v)[8], float fill = 0.0f) {
   const int c = chunk_column(i, t, threads);
   uint2 w = make_uint2(0, 0);
   float s = 0.0f;
@@ -366,7 +366,7 @@ __device__ __forceinline__ void ckpt_load_chunk(const uint8_t* codes, const uint
   ckpt_values4<FMT>(w.y, s, v + 4);
   if (!VEC) {  // 0 times a group's NaN is none of the row's padding
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < K ? v[j] : 0.0f;
+    for (int j = 0; j < 8; ++j) v[j] = c + j < K ? v[j] : fill;
   }
 }
 
