@@ -38,6 +38,7 @@ constexpr int kSMs = 148;
 constexpr int kTileCols = 64;          // of X per warp step, 16 rows (bf16) or 32
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kSBytes = 96 * 1024;    // of S in shared memory at a time
+constexpr int kMaxY = 65535;          // of a grid's y
 constexpr int kMaxRows = 512;         // of one warp between two joins
 
 struct WgradParams {
@@ -48,6 +49,7 @@ struct WgradParams {
   int M, K, r;
   int col_warps;          // 1, 2 or 4; the others of the 16 warps share out the rows
   int rows;               // per CTA, a multiple of a step's rows
+  int parts, zs;          // of the rows, of the columns of S
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -146,16 +148,20 @@ __device__ __forceinline__ void pair_rows(uint32_t at_a, uint32_t at_b, uint32_t
   }
 }
 
-// NT: columns of S per CTA in tiles of 8.  blockIdx: x columns of X, y CTA of the rows, z columns of S.
+// NT: columns of S per CTA in tiles of 8.  blockIdx: x columns of X, y part of the rows, z columns of S (and once
+// more for each kMaxY parts that tall X have).
 template <int SRC, int NT>
 __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(WgradParams p) {
   extern __shared__ __align__(128) uint8_t smem[];  // S, then the rings; at the end the warps' sums
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int cw = warp % p.col_warps, rw = warp / p.col_warps, row_warps = kWarps / p.col_warps;
+  int part = blockIdx.y, z = blockIdx.z;
+  while (z >= p.zs) z -= p.zs, part += kMaxY;  // seldom: no division
+  if (part >= p.parts) return;
   const int k0 = (blockIdx.x * p.col_warps + cw) * kTileCols;
-  const int n0 = blockIdx.z * NT * 8;
-  const int row0 = blockIdx.y * p.rows, row_end = min(p.M, row0 + p.rows);
+  const int n0 = z * NT * 8;
+  const int row0 = part * p.rows, row_end = min(p.M, row0 + p.rows);
   const int groups = (p.K + kCkptGroup - 1) / kCkptGroup;
   const uint32_t s_tile = smem_u32(smem);
   const uint32_t ring = s_tile + kSBytes + warp * Tile<SRC>::stages * Tile<SRC>::bytes;
@@ -319,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(WgradParams p) {
   constexpr int kPitch = NT * 8 + 2;
   const int cols = p.col_warps * kTileCols;
   float* sums = reinterpret_cast<float*>(smem);
-  float* out = p.out + static_cast<size_t>(blockIdx.y) * p.K * p.r;
+  float* out = p.out + static_cast<size_t>(part) * p.K * p.r;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -388,7 +394,7 @@ svdq_status launch(const WgradParams& p, const Plan& q, cudaStream_t stream) {
   const size_t smem = std::max(loop, join);
   static std::atomic<uint64_t> allowed{0};
   SVDQ_TRY(allow_dynamic_smem(reinterpret_cast<const void*>(wgrad_kernel<SRC, NT>), static_cast<int>(smem), allowed));
-  wgrad_kernel<SRC, NT><<<dim3(q.blocks, q.parts, q.zs), kThreads, smem, stream>>>(p);
+  wgrad_kernel<SRC, NT><<<dim3(q.blocks, std::min(q.parts, kMaxY), q.zs * ((q.parts + kMaxY - 1) / kMaxY)), kThreads, smem, stream>>>(p);
   SVDQ_CUDA_TRY(cudaGetLastError());
   return SVDQ_OK;
 }
@@ -412,10 +418,8 @@ size_t lowrank_wgrad_workspace(int M, int K, int r) {
 svdq_status launch_lowrank_wgrad(const void* X, const uint8_t* scales, int src, const void* S, int M, int K, int r,
                                  float* G, void* workspace, cudaStream_t stream) {
   const Plan q = plan(M, K, r, src ? Tile<1>::rows : Tile<0>::rows);
-  if (q.parts > 65535 || q.blocks > 0x7FFFFFFF / 8)
-    return fail(SVDQ_ERR_INVALID_ARG, "M=%d rows of K=%d are too many", M, K);
   WgradParams p{static_cast<const uint8_t*>(X), scales, static_cast<const uint16_t*>(S),
-                q.parts > 1 ? static_cast<float*>(workspace) : G, M, K, r, q.col_warps, q.rows};
+                q.parts > 1 ? static_cast<float*>(workspace) : G, M, K, r, q.col_warps, q.rows, q.parts, q.zs};
   SVDQ_TRY(src == 0 ? launch_nt<0>(p, q, stream) : src == 1 ? launch_nt<1>(p, q, stream) : launch_nt<2>(p, q, stream));
   if (q.parts > 1) {
     const size_t n = static_cast<size_t>(K) * r;
