@@ -149,6 +149,7 @@ svdq_status upload_lowrank(svdq_weights* w, cudaStream_t stream) {
   cudaFree(w->d_L2t);
   w->d_L1t = w->d_L2t = nullptr;
   w->r_pad = rp;
+  w->branch_exp = -1000;
   if (rp == 0) return SVDQ_OK;
   std::vector<uint16_t> l1t(static_cast<size_t>(rp) * K, 0), l2t(static_cast<size_t>(N) * rp, 0);
   for (int k = 0; k < K; ++k)
@@ -159,6 +160,19 @@ svdq_status upload_lowrank(svdq_weights* w, cudaStream_t stream) {
       const float v = bf16_to_f32(w->L2[static_cast<size_t>(i) * N + n]);
       l2t[static_cast<size_t>(n) * rp + i] = f32_to_bf16_rne(static_cast<float>(v * inv_aw));  // exact
     }
+  // |T| <= max|x| s1 and |T L2 / alpha_w| <= |T| s2 with the largest absolute sums of a row of L1^T and of L2^T
+  auto largest_sum = [](const std::vector<uint16_t>& v, size_t row) {
+    double most = 0;
+    for (size_t at = 0; at < v.size(); at += row) {
+      double sum = 0;
+      for (size_t i = at; i < at + row; ++i)
+        if ((v[i] & 0x7F80) != 0x7F80) sum += std::fabs(bf16_to_f32(v[i]));  // not of infinities and NaNs
+      most = std::max(most, sum);
+    }
+    return most;
+  };
+  const double s1 = largest_sum(l1t, K), s2 = largest_sum(l2t, rp);
+  if (s1 > 0) w->branch_exp = std::ilogb(s1 * std::max(s2, 1.0)) + 1;
   SVDQ_CUDA_TRY(cudaMalloc(&w->d_L1t, l1t.size() * 2));
   SVDQ_CUDA_TRY(cudaMalloc(&w->d_L2t, l2t.size() * 2));
   SVDQ_CUDA_TRY(cudaMemcpyAsync(w->d_L1t, l1t.data(), l1t.size() * 2, cudaMemcpyHostToDevice, stream));

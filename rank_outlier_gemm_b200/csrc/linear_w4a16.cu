@@ -59,6 +59,8 @@ struct W4A16Params {
   float* T;               // [splits of K][M][r_pad]
   int M, N, K, r_pad, steps, tiles, t_splits;
   int groups, cluster, blocks;  // of steps; CTAs that share an output; pairs of units
+  int branch_exp;               // |T| max |L2 / alpha_w| over the token's scale stay finite while the scale's (biased)
+                                // exponent is at least this and that of the largest |x| together
   float alpha_w;
 };
 
@@ -82,6 +84,12 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
 
+// The larger magnitudes of two bf16 pairs, with any sign; a NaN does not count.
+__device__ __forceinline__ uint32_t larger_pair(uint32_t a, uint32_t b) {
+  uint32_t m;
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  return m;
+}
 // What rounding to `hi` left of v; nothing of an infinity or a NaN, which stays in hi alone.
 __device__ __forceinline__ float rest(float v, float hi) { return isfinite(hi) ? v - hi : 0.0f; }
 
@@ -133,6 +141,7 @@ __global__ void __launch_bounds__(kPrepThreads) w4a16_prepare_kernel(W4A16Params
     const uint16_t* x = p.X + static_cast<size_t>(m) * p.K;
     // xh of columns 8 c..8 c + 7, 0 beyond K; the first kHeld chunks of a thread stay in registers
     constexpr int kHeld = 4;
+    uint32_t raw = 0;  // the largest magnitudes of x at even and at odd places, of any sign
     auto chunk = [&](int c, float (&v)[8]) {
       uint4 w = make_uint4(0, 0, 0, 0);
       float f[8] = {};
@@ -141,6 +150,7 @@ __global__ void __launch_bounds__(kPrepThreads) w4a16_prepare_kernel(W4A16Params
         load8(p.inv_lam + c * 8, f);
       }
       unpack8(w, v, static_cast<const __nv_bfloat16*>(nullptr));
+      raw = larger_pair(larger_pair(raw, larger_pair(w.x, w.y)), larger_pair(w.z, w.w));
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= f[j];
     };
@@ -163,12 +173,15 @@ __global__ void __launch_bounds__(kPrepThreads) w4a16_prepare_kernel(W4A16Params
       chunk(c, v);
       note(v);
     }
-    top = __reduce_max_sync(0xffffffffu, top);
-    uint32_t* r = reinterpret_cast<uint32_t*>(red);
-    if (lane == 0) r[warp] = top;
+    // the token's scale 2^(e - 127), a normal number: brings the largest xh to [2^13, 2^14), or is as large as the
+    // branch needs it, where x inv_lam is a hundred binary orders below x
+    const int ex = static_cast<int>(max(raw >> 7 & 0xFF, raw >> 23 & 0xFF));
+    int e = max(max(static_cast<int>(top >> 23) - 13, ex + p.branch_exp), 1);
+    e = __reduce_max_sync(0xffffffffu, e);
+    int* r = reinterpret_cast<int*>(red);
+    if (lane == 0) r[warp] = e;
     __syncthreads();
-    top = __reduce_max_sync(0xffffffffu, lane < kPrepWarps ? r[lane] : 0u);
-    const int e = max(static_cast<int>(top >> 23) - 13, 1);  // biased: the scale is 2^(e - 127), a normal number
+    e = min(__reduce_max_sync(0xffffffffu, lane < kPrepWarps ? r[lane] : 1), 253);
     const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
     if (threadIdx.x == 0) p.pow2[m] = __uint_as_float(static_cast<uint32_t>(e) << 23);
     auto place = [&](int c, const float (&v)[8]) {
@@ -629,6 +642,7 @@ svdq_status launch_w4a16(const svdq_weights* w, const void* X, int M, void* Y, v
   p.t_splits = (w->K + kTSplit - 1) / kTSplit;
   p.groups = step_groups(w->N, p.steps);
   p.alpha_w = w->alpha_w;
+  p.branch_exp = w->branch_exp - 124;  // |T L2 / alpha_w| <= 2^(ex - 126 + branch_exp), at most 2^125 over the scale
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.frag = reinterpret_cast<uint4*>(ws);
   ws += up256(static_cast<size_t>(p.steps) * p.tiles * 4 * 32 * 16);

@@ -199,6 +199,7 @@ struct svdq_weights {
   int rank = 0;       // SVD rank + LoRA ranks
   int r_pad = 0;      // rank rounded up to 16
   float alpha_w = 1.0f;
+  int branch_exp = -1000;  // |T L2 / alpha_w| and |T| are below 2^branch_exp times the token's largest |x|
   uint8_t* d_wq = nullptr;       // [N, K/2]
   uint8_t* d_wsf = nullptr;      // NVFP4: [ceil(N/128)*128, K/16] atom layout;
                                  // INT4: bf16 [K/64][round_up(N, 256)]
