@@ -532,7 +532,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT > 2 ? 2 : 3) w4a16_kernel(W4A1
     auto finish = [&](int i, float v) {
       const int m = i / kRows, row = i % kRows, n = unit_row<INT4>(unit0 + row / kUnitRows, (row >> 3) & 3, row & 7);
       if (n >= p.N) return;
-      const __nv_bfloat16 y = __float2bfloat16_rn(__fmaf_rn(v, p.pow2[m] * p.alpha_w, __ldg(p.bias + n)));
+      // the sum times alpha_w first: the product of the two powers of two may leave fp32's range where Y does not
+      const __nv_bfloat16 y = __float2bfloat16_rn(__fmaf_rn(v * p.alpha_w, p.pow2[m], __ldg(p.bias + n)));
       p.Y[static_cast<size_t>(m) * p.N + n] = *reinterpret_cast<const uint16_t*>(&y);
     };
     if (p.cluster == 1) {

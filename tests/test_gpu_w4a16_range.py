@@ -41,3 +41,19 @@ def test_tokens_that_the_smoothing_leaves_nothing_of(fmt, factor, scale):
     y = run(w, X).double().cpu().numpy()
     assert np.isfinite(y).all()
     assert np.all(np.abs(y - ref) <= near + 2.0 ** -8 * (np.abs(ref) + near))
+
+
+@pytest.mark.parametrize("alpha,x", [(2.0 ** -100, 2.0 ** -37), (2.0 ** -60, 2.0 ** -80), (2.0 ** -40, 1.0), (2.0 ** -14, 1.0),
+                                     (2.0 ** 20, 2.0 ** 60), (2.0 ** 40, 2.0 ** 60)])
+def test_factors_of_the_weights_at_the_ends_of_the_range(alpha, x):
+    """Every weight is 6 * 448 alpha_w and every activation x: Y is exact.  alpha_w times the token's power of two
+    (x 2^-13) leaves fp32's range at the first two, where Y is 2^-116 and 2^-119."""
+    N, K = 16, 1024
+    w = lib().svdq_weights_from_codes(N, K, 0, alpha, np.full((N, K // 2), 0x77, np.uint8), np.full(128 * K // 16, 0x7E, np.uint8),
+                                      np.ones(K, np.float32), None, None, None, fmt="nvfp4")
+    X = torch.full((3, K), x, dtype=torch.bfloat16, device="cuda")
+    X[1] = 0.0
+    X[2, 1:] = 0.0
+    want = X.double().sum(1, keepdim=True) * 2688.0 * alpha
+    assert float(want[0, 0]) > 2.0 ** -120
+    assert torch.equal(run(w, X).double(), want.expand(3, N))
