@@ -418,8 +418,8 @@ svdq_status svdq_layer_norm(const svdq_norm_desc* desc, const void* Z, const voi
  *           bytes (NULL if that is 0); calls that may run at the same time need
  *           one each
  * The column sums are joined in a fixed order: equal calls give equal bits.  A
- * wait that runs out is recorded in the device error word; the outputs of that
- * call are then unspecified.
+ * wait that runs out is recorded in the device error word; dscale and dshift of
+ * that call are then unspecified, and rows of dZ may be left as they were.
  */
 svdq_status svdq_layer_norm_backward(const svdq_norm_desc* desc, const void* dY, const void* Z, const void* codes,
                                      const void* scales, int ckpt_format, const float* stats, const void* scale,
@@ -527,6 +527,17 @@ svdq_status svdq_check_device_errors(void* stream);
  */
 svdq_status svdq_debug_launch_stalled_act(const svdq_weights* w, const void* X_bf16, int M,
                                           void* xq, void* xsf, void* T, void* stream);
+
+/*
+ * Test hook: svdq_layer_norm_backward from Z, without scale, on a ring whose
+ * stages never fill, so that its waits run out after svdq_set_wait_limit_ns and
+ * it ends with SVDQ_ERR_TIMEOUT in the device error word and without a store to
+ * dZ.  SVDQ_ERR_INVALID_ARG where rows are not read in whole pieces (no waits);
+ * otherwise as there.
+ */
+svdq_status svdq_debug_stalled_layer_norm_backward(const svdq_norm_desc* desc, const void* dY, const void* Z,
+                                                   const float* stats, void* dZ, float* dscale, float* dshift,
+                                                   void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Test hook: svdq_linear_w4a4 with the split-K factor fixed to `ksplit` CTAs

@@ -97,6 +97,7 @@ _SIGS = {
     "svdq_search_alpha": (_i, [_vp, _vp, _i, _vp, _i, _i, _vp, _i, ctypes.POINTER(PrepareOpts), _vp,
                                ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i)]),
     "svdq_debug_launch_stalled_act": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp]),
+    "svdq_debug_stalled_layer_norm_backward": (_i, [_desc, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "svdq_debug_linear_w4a4_ksplit": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _i, _vp]),
     "svdq_debug_forward_small_m": (_i, [_vp, _vp, _i, _vp, _i, _vp]),
     "svdq_last_error": (ctypes.c_char_p, []),
@@ -341,6 +342,23 @@ def svdq_debug_launch_stalled_act(w: Weights, X, xq, xsf, T, stream=None) -> Non
 def svdq_linear_w4a4(w: Weights, xq, xsf, T, M: int, Y: torch.Tensor, stream=None) -> None:
     _check(_lib.svdq_linear_w4a4(w.handle, _dev(xq, "xq"), _dev(xsf, "xsf"), _dev(T, "T"), M, _dev(Y, "Y"),
                                  _stream(stream)), "svdq_linear_w4a4")
+
+
+def svdq_debug_stalled_layer_norm_backward(dY, Z, stats, dZ, dscale, dshift, workspace, group_rows: int = 0,
+                                           stream=None) -> None:
+    dev, s = _device_and_stream(stream)
+    M, K = _shape2(dY, "dY")
+    dyp, ld_dy = _rows_arg(dY, "dY", (M, K), DTYPES, dev)
+    zp, ld_z = _rows_arg(Z, "Z", (M, K), (dY.dtype,), dev)
+    dzp, ld_dz = _rows_arg(dZ, "dZ", (M, K), (dY.dtype,), dev)
+    shape = (-(-M // (group_rows or M)), K)
+    da = _arg(dscale, "dscale", shape, torch.float32, dev) if dscale is not None else None
+    dc = _arg(dshift, "dshift", shape, torch.float32, dev) if dshift is not None else None
+    stp = _arg(stats, "stats", (M, 2), torch.float32, dev)
+    ws, n = _workspace(workspace, dev)
+    d = _norm_desc(M, K, group_rows, DTYPES[dY.dtype], 2, False, 0.0, ld_z, 0, ld_dy, ld_dz, 0)
+    _check(_lib.svdq_debug_stalled_layer_norm_backward(d, dyp, zp, stp, dzp, da, dc, ws, n, s),
+           "svdq_debug_stalled_layer_norm_backward")
 
 
 def svdq_debug_linear_w4a4_ksplit(w: Weights, xq, xsf, T, M: int, Y: torch.Tensor, ksplit: int,

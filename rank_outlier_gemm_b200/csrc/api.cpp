@@ -956,6 +956,24 @@ svdq_status svdq_layer_norm_backward(const svdq_norm_desc* desc, const void* dY,
                                     static_cast<cudaStream_t>(stream));
 }
 
+svdq_status svdq_debug_stalled_layer_norm_backward(const svdq_norm_desc* desc, const void* dY, const void* Z,
+                                                   const float* stats, void* dZ, float* dscale, float* dshift,
+                                                   void* workspace, size_t workspace_bytes, void* stream) {
+  NormArgs a;
+  SVDQ_TRY(norm_args(desc, &a));
+  SVDQ_TRY(check_elem_ptr(dY, a.dtype, "dY"));
+  SVDQ_TRY(check_elem_ptr(Z, a.dtype, "Z"));
+  SVDQ_TRY(check_dev_ptr(stats, "stats"));
+  SVDQ_TRY(check_elem_ptr(dZ, a.dtype, "dZ"));
+  if (dscale) SVDQ_TRY(check_elem_ptr(dscale, SVDQ_DTYPE_FP32, "dscale"));
+  if (dshift) SVDQ_TRY(check_elem_ptr(dshift, SVDQ_DTYPE_FP32, "dshift"));
+  SVDQ_TRY(check_workspace(workspace, workspace_bytes, layer_norm_backward_workspace(a.M, a.K, a.rows)));
+  SVDQ_TRY(check_device());
+  a.stall = 1;
+  return launch_layer_norm_backward(a, dY, Z, nullptr, nullptr, 0, stats, nullptr, dZ, dscale, dshift, workspace,
+                                    static_cast<cudaStream_t>(stream));
+}
+
 svdq_status svdq_ckpt8_encode(const void* X, int dtype, int M, int K, int64_t ld, int format, void* codes,
                               void* scales, void* stream) {
   SVDQ_TRY(check_rows(M, K, 1 << 30));

@@ -40,8 +40,10 @@ constexpr int kSMs = 148;
 __device__ __forceinline__ void team_barrier(int team, int warps) {
   asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(warps * 32) : "memory");
 }
-// Of a and b: lanes 0-15 of the result hold the first sum, lanes 16-31 the second.
-__device__ __forceinline__ float team_sum_halves(float a, float b, int warps, int team, float* red, int& turn) {
+// Of a and b: lanes 0-15 of the result hold the first sum, lanes 16-31 the second.  `flag`, if given, is read
+// behind the barrier into `seen`.
+__device__ __forceinline__ float team_sum_halves(float a, float b, int warps, int team, float* red, int& turn,
+                                                 const volatile int* flag = nullptr, int* seen = nullptr) {
   float v = warp_sum2_halves(a, b);
   if (warps == 1) return v;
   const int lane = threadIdx.x & 31;
@@ -49,13 +51,15 @@ __device__ __forceinline__ float team_sum_halves(float a, float b, int warps, in
   turn ^= 1;
   if ((lane & 15) == 0) r[lane + (threadIdx.x >> 5) - team * warps] = v;
   team_barrier(team, warps);
+  if (flag) *seen = *flag;
   v = (lane & 15) < warps ? r[lane] : 0.0f;
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ float2 team_sum2(float a, float b, int warps, int team, float* red, int& turn) {
-  const float v = team_sum_halves(a, b, warps, team, red, turn);
+__device__ __forceinline__ float2 team_sum2(float a, float b, int warps, int team, float* red, int& turn,
+                                            const volatile int* flag = nullptr, int* seen = nullptr) {
+  const float v = team_sum_halves(a, b, warps, team, red, turn, flag, seen);
   const float o = __shfl_xor_sync(0xffffffffu, v, 16);
   return (threadIdx.x & 16) ? make_float2(o, v) : make_float2(v, o);
 }
@@ -196,6 +200,7 @@ struct BwdParams {
   float one;
   int* err;
   uint64_t wait_ns;
+  int stall;              // test hook: one arrival more than the ring's stages get
 };
 
 constexpr int kMaxStages = 4;
@@ -250,7 +255,7 @@ __global__ void __launch_bounds__(32 * (kBackwardWarps + 1)) layer_norm_backward
     if (threadIdx.x == 0) {
       s_abort = 0;
       for (int s = 0; s < p.stages; ++s) {
-        mbar_init(&full[s], 33);
+        mbar_init(&full[s], 33 + p.stall);
         mbar_init(&empty[s], workers / 32);
       }
       fence_barrier_init();
@@ -297,6 +302,12 @@ __global__ void __launch_bounds__(32 * (kBackwardWarps + 1)) layer_norm_backward
         copies_arrive(bar);
         if (++stage == p.stages) stage = 0, parity ^= 1;
       }
+      // None of these copies may land after the CTA has ended, which the teams alone do not see to once a wait ran
+      // out.  The stages below `stage` were filled in this pass, the others in the one before (or not at all).
+      WaitCtl drain = ctl;
+      int none = 0;
+      drain.abort = &none;
+      for (int s = 0; s < p.stages; ++s) wait_warp(&full[s], s < stage ? parity ^ 1 : parity, drain);
       return;
     }
   }
@@ -338,7 +349,9 @@ __global__ void __launch_bounds__(32 * (kBackwardWarps + 1)) layer_norm_backward
   }
   uint32_t parity = 0;
   int stage = 0;
-  bool alive = true;  // false once a wait ran out: the error word says so, the results are garbage
+  // False once a wait ran out (the error word says so) or the CTA gave up: the teams then go through their rows
+  // without freeing stages or storing, so that their barriers still match.
+  bool alive = true;
   for (int m = m0 + team, block = m0; block < last; block += step, m += step) {
     const uint8_t* here = ring + stage * at.bytes;
     if (VEC) alive = wait_warp(&full[stage], parity, ctl) && alive;
@@ -407,9 +420,10 @@ __global__ void __launch_bounds__(32 * (kBackwardWarps + 1)) layer_norm_backward
       unpack2(s2, a2, b2);
       if (VEC && kHeld == NV) {  // the row is in registers
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (lane == 0 && alive) mbar_arrive(&empty[stage]);
       }
-      const float2 s = team_sum2(a1 + b1, a2 + b2, p.warps, team, red[team], turn);
+      int aborted = VEC && !alive;  // or any other warp of the team
+      const float2 s = team_sum2(a1 + b1, a2 + b2, p.warps, team, red[team], turn, VEC ? &s_abort : nullptr, &aborted);
       const F2 m1 = f2(-s.x * inv_k, -s.x * inv_k), m2 = f2(-s.y * inv_k, -s.y * inv_k), rs = f2(rstd, rstd);
       T* dz = static_cast<T*>(p.dZ) + m * p.ld_dz;
 #pragma unroll
@@ -425,25 +439,17 @@ __global__ void __launch_bounds__(32 * (kBackwardWarps + 1)) layer_norm_backward
         float v[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) unpack2(mul2(rs, fma2(xh[j], m2, add2(gi[j], m1))), v[2 * j], v[2 * j + 1]);
-        store_chunk<T, VEC>(dz, p.K, i, t, threads, v);
+        if (!aborted) store_chunk<T, VEC>(dz, p.K, i, t, threads, v);
       }
       if (VEC && kHeld != NV) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (lane == 0 && alive) mbar_arrive(&empty[stage]);
       }
-    } else if (VEC && lane == 0) {
+    } else if (VEC && lane == 0 && alive) {
       mbar_arrive(&empty[stage]);
     }
     if (++stage == p.stages) stage = 0, parity ^= 1;
   }
-  // after a wait that ran out, nothing may still be on its way when the CTA ends
-  if (VEC && threadIdx.x == 0 && s_abort) {
-    WaitCtl drain = ctl;
-    int none = 0;
-    drain.abort = &none;
-    for (int s = 0; s < p.stages; ++s) wait_bounded(&full[s], s < stage ? parity : parity ^ 1, drain);
-  }
-
   float fa[NV][8], fc[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -456,6 +462,7 @@ __global__ void __launch_bounds__(32 * (kBackwardWarps + 1)) layer_norm_backward
   float* out_a = p.partial ? p.partial + static_cast<size_t>(blockIdx.x) * 2 * p.K
                            : p.dscale ? p.dscale + static_cast<size_t>(group) * p.K : nullptr;
   float* out_c = p.partial ? out_a + p.K : p.dshift ? p.dshift + static_cast<size_t>(group) * p.K : nullptr;
+  if (VEC && *static_cast<volatile int*>(&s_abort)) out_a = out_c = nullptr;
   if (teams > 1) {  // the teams' sums side by side, then added in order
     float* sums = smem;  // [teams][2][K]
     workers_barrier(workers);  // the multipliers and the ring are done with
@@ -677,11 +684,12 @@ svdq_status launch_layer_norm_backward(const NormArgs& a, const void* dY, const 
   const Shape s = backward_shape(a.K, a.rows);
   BwdParams p{dY, Z, codes, scales, reinterpret_cast<const float2*>(stats), scale, dZ, dscale, dshift, nullptr,
               a.ld_z, a.ld_dy, a.ld_dz, a.ld_param, a.M, a.K, a.rows, backward_splits(a.K, a.rows, groups),
-              a.param_dtype, s.warps, s.teams, 0, 0, a.plus_one ? 1.0f : 0.0f, nullptr, 0};
+              a.param_dtype, s.warps, s.teams, 0, 0, a.plus_one ? 1.0f : 0.0f, nullptr, 0, a.stall};
   if (p.splits > 1 && (dscale || dshift)) p.partial = static_cast<float*>(workspace);
   const bool vec = vector_rows(a.K, {dY, Z, codes, scale, dZ, p.partial ? nullptr : dscale, p.partial ? nullptr : dshift},
                                {a.ld_z, a.ld_dy, a.ld_dz, a.ld_param}) &&
                    (!codes || a.K % 16 == 0);  // bulk copies of whole rows of codes
+  if (a.stall && !vec) return fail(SVDQ_ERR_INVALID_ARG, "rows of this layout are read without a wait");
   const int src = !codes ? 0 : ckpt == SVDQ_CKPT8_INT8 ? 1 : 2;
   svdq_status st;
   switch (a.dtype) {

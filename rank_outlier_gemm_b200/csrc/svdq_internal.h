@@ -147,6 +147,7 @@ struct NormArgs {
   int M, K, rows, dtype, param_dtype, plus_one;
   float eps;
   int64_t ld_z, ld_y, ld_dy, ld_dz, ld_param;
+  int stall = 0;  // test hook of the gradient: waits that never complete
 };
 constexpr int kNormMaxK = 16384;
 svdq_status launch_layer_norm(const NormArgs& a, const void* Z, const void* scale, const void* shift, void* Y,
