@@ -8,6 +8,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <new>
 
 #include "svdq_internal.h"
 
@@ -308,51 +309,55 @@ svdq_status build_from_codes(int N, int K, int rank, float alpha_w, const uint8_
     delete w;
     return s;
   };
-  cudaGetDevice(&w->device);
-  w->N = N;
-  w->K = K;
-  w->rank = rank;
-  w->format = format;
-  w->alpha_w = alpha_w;
-  w->inv_lam.assign(inv_lam, inv_lam + K);
-  if (rank > 0) {
-    w->L1p.assign(L1p, L1p + static_cast<size_t>(K) * rank);
-    w->L2.assign(L2, L2 + static_cast<size_t>(rank) * N);
+  try {  // no exception leaves a C entry point
+    cudaGetDevice(&w->device);
+    w->N = N;
+    w->K = K;
+    w->rank = rank;
+    w->format = format;
+    w->alpha_w = alpha_w;
+    w->inv_lam.assign(inv_lam, inv_lam + K);
+    if (rank > 0) {
+      w->L1p.assign(L1p, L1p + static_cast<size_t>(K) * rank);
+      w->L2.assign(L2, L2 + static_cast<size_t>(rank) * N);
+    }
+    w->bias.assign(N, 0.0f);
+    if (bias) std::copy(bias, bias + N, w->bias.begin());
+    std::vector<float> bias_pad(static_cast<size_t>(round_up(N, 256)), 0.0f);
+    std::copy(w->bias.begin(), w->bias.end(), bias_pad.begin());
+    const size_t nk = static_cast<size_t>(N) * K;
+    const int npad = scale_rows(N, format);
+    std::vector<uint8_t> scales;
+    if (format == SVDQ_FORMAT_INT4) {
+      scales.assign(sf, sf + static_cast<size_t>(K / 64) * npad * 2);
+      for (int g = 0; g < K / 64; ++g)
+        std::fill(scales.begin() + (static_cast<size_t>(g) * npad + N) * 2,
+                  scales.begin() + static_cast<size_t>(g + 1) * npad * 2, uint8_t{0});
+    } else {
+      scales.assign(sf, sf + static_cast<size_t>(npad) * (K / 16));
+      for (int n = N; n < npad; ++n)
+        for (int c = 0; c < K / 16; ++c) scales[sf_atom_index(n, c, K)] = 0;
+    }
+    cudaError_t e = cudaSuccess;
+    auto upload = [&](auto** dst, const void* src, size_t bytes) {
+      if (e == cudaSuccess) e = cudaMalloc(dst, bytes);
+      if (e == cudaSuccess) e = cudaMemcpyAsync(*dst, src, bytes, cudaMemcpyHostToDevice, stream);
+    };
+    upload(&w->d_wq, codes, nk / 2);
+    upload(&w->d_wsf, scales.data(), scales.size());
+    upload(&w->d_inv_lam, inv_lam, static_cast<size_t>(K) * 4);
+    upload(&w->d_bias, bias_pad.data(), bias_pad.size() * 4);
+    const cudaError_t synced = cudaStreamSynchronize(stream);  // the host copies end with this call
+    if (e == cudaSuccess) e = synced;
+    if (e != cudaSuccess) return bail(cuda_fail(e, "upload of the weights"));
+    svdq_status st = upload_lowrank(w, stream);
+    if (st == SVDQ_OK) st = make_weight_maps(w);
+    if (st != SVDQ_OK) return bail(st);
+    *out = w;
+    return SVDQ_OK;
+  } catch (const std::bad_alloc&) {
+    return bail(fail(SVDQ_ERR_OOM, "host allocation failed"));
   }
-  w->bias.assign(N, 0.0f);
-  if (bias) std::copy(bias, bias + N, w->bias.begin());
-  std::vector<float> bias_pad(static_cast<size_t>(round_up(N, 256)), 0.0f);
-  std::copy(w->bias.begin(), w->bias.end(), bias_pad.begin());
-  const size_t nk = static_cast<size_t>(N) * K;
-  const int npad = scale_rows(N, format);
-  std::vector<uint8_t> scales;
-  if (format == SVDQ_FORMAT_INT4) {
-    scales.assign(sf, sf + static_cast<size_t>(K / 64) * npad * 2);
-    for (int g = 0; g < K / 64; ++g)
-      std::fill(scales.begin() + (static_cast<size_t>(g) * npad + N) * 2,
-                scales.begin() + static_cast<size_t>(g + 1) * npad * 2, uint8_t{0});
-  } else {
-    scales.assign(sf, sf + static_cast<size_t>(npad) * (K / 16));
-    for (int n = N; n < npad; ++n)
-      for (int c = 0; c < K / 16; ++c) scales[sf_atom_index(n, c, K)] = 0;
-  }
-  cudaError_t e = cudaSuccess;
-  auto upload = [&](auto** dst, const void* src, size_t bytes) {
-    if (e == cudaSuccess) e = cudaMalloc(dst, bytes);
-    if (e == cudaSuccess) e = cudaMemcpyAsync(*dst, src, bytes, cudaMemcpyHostToDevice, stream);
-  };
-  upload(&w->d_wq, codes, nk / 2);
-  upload(&w->d_wsf, scales.data(), scales.size());
-  upload(&w->d_inv_lam, inv_lam, static_cast<size_t>(K) * 4);
-  upload(&w->d_bias, bias_pad.data(), bias_pad.size() * 4);
-  const cudaError_t synced = cudaStreamSynchronize(stream);  // the host copies end with this call
-  if (e == cudaSuccess) e = synced;
-  if (e != cudaSuccess) return bail(cuda_fail(e, "upload of the weights"));
-  svdq_status st = upload_lowrank(w, stream);
-  if (st == SVDQ_OK) st = make_weight_maps(w);
-  if (st != SVDQ_OK) return bail(st);
-  *out = w;
-  return SVDQ_OK;
 }
 
 svdq_status check_shape(int N, int K) {
