@@ -161,18 +161,16 @@ svdq_status upload_lowrank(svdq_weights* w, cudaStream_t stream) {
       const float v = bf16_to_f32(w->L2[static_cast<size_t>(i) * N + n]);
       l2t[static_cast<size_t>(n) * rp + i] = f32_to_bf16_rne(static_cast<float>(v * inv_aw));  // exact
     }
-  // |T| <= max|x| s1 and |T L2 / alpha_w| <= |T| s2 with the largest absolute sums of a row of L1^T and of L2^T
-  auto largest_sum = [](const std::vector<uint16_t>& v, size_t row) {
-    double most = 0;
-    for (size_t at = 0; at < v.size(); at += row) {
-      double sum = 0;
-      for (size_t i = at; i < at + row; ++i)
-        if ((v[i] & 0x7F80) != 0x7F80) sum += std::fabs(bf16_to_f32(v[i]));  // not of infinities and NaNs
-      most = std::max(most, sum);
+  // |T| <= max|x| s1 and |T L2 / alpha_w| <= |T| s2, with s the length of a row times the largest finite magnitude
+  auto largest = [](const std::vector<uint16_t>& v) {
+    int16_t most = 0;  // signed, which every x86 compares 8 at a time
+    for (const uint16_t bits : v) {
+      const int16_t m = static_cast<int16_t>(bits & 0x7FFF), finite = m < 0x7F80 ? m : int16_t{0};
+      most = most > finite ? most : finite;
     }
-    return most;
+    return static_cast<double>(bf16_to_f32(static_cast<uint16_t>(most)));
   };
-  const double s1 = largest_sum(l1t, K), s2 = largest_sum(l2t, rp);
+  const double s1 = K * largest(l1t), s2 = rp * largest(l2t);
   if (s1 > 0) w->branch_exp = std::ilogb(s1 * std::max(s2, 1.0)) + 1;
   SVDQ_CUDA_TRY(cudaMalloc(&w->d_L1t, l1t.size() * 2));
   SVDQ_CUDA_TRY(cudaMalloc(&w->d_L2t, l2t.size() * 2));
