@@ -358,9 +358,9 @@ svdq_status svdq_forward_noalloc(const svdq_weights* w, const void* X_bf16, int 
  * decoder, the modulation layers of a DiT block whose input is one embedding
  * per image):
  * Y = bf16_rne(alpha_w * (sum_k fp32(x * inv_lam) deq(wq) + T (L2 / alpha_w)) + b),
- * T = X L1', sums in fp32.  The activations are not quantized (they enter as
- * 22-bit values), the weights are those of svdq_linear_w4a4; each is read once
- * for all tokens.  1 <= M <= 16: for more tokens use svdq_forward.  A token's
+ * T = X L1', sums in fp32, T in fp32.  The activations are not quantized (x inv_lam
+ * enters with 22 bits, and no finer than 2^-38 of the token's largest), the weights
+ * are those of svdq_linear_w4a4; each is read once for all tokens.  1 <= M <= 16: for more tokens use svdq_forward.  A token's
  * result does not depend on the other tokens of the call.
  *   X_bf16  device, M x K bf16          Y_bf16  device, M x N bf16
  *   workspace  device memory of at least svdq_linear_w4a16_workspace_bytes(w, M)
@@ -444,7 +444,12 @@ size_t svdq_layer_norm_backward_workspace_bytes(int M, int K, int group_rows);
 svdq_status svdq_ckpt8_encode(const void* X, int dtype, int M, int K, int64_t ld, int format, void* codes,
                               void* scales, void* stream);
 
-/* The values of a checkpoint, code * scale, rounded once to dtype. */
+/*
+ * The values of a checkpoint, code * scale, rounded once to dtype.  In fp16 that
+ * rounds a value next to the type's largest to an infinity: the encoder's code of a
+ * magnitude from 63488 (E4M3) or, in a group that reaches 65280, from 65024 (INT8)
+ * stands for 65536.
+ */
 svdq_status svdq_ckpt8_decode(const void* codes, const void* scales, int M, int K, int format, void* X, int dtype,
                               int64_t ld, void* stream);
 

@@ -12,10 +12,11 @@
 // second kernel adds them in a fixed order (no atomics: equal calls give equal bits).
 //
 // Measured (one B200, device time in a graph; the copy rate would take the time in brackets): forward
-// bf16 8192 x 4096 43 us (20.5), fp32 53 (40.9), bf16 4096 x 1152 with an int8 checkpoint 10.2 (3.6); gradient
-// bf16 8192 x 4096 38 (30.7), 4500 x 4096 from an int8 checkpoint 26.2 (14.2), 8192 x 640 12.9 (4.8).  The
-// 16-bit forward and decoding issue for half of their time, and the rest is a row's chain of two reductions
-// with 32 warps per SM to cover it.
+// bf16 8192 x 4096 43.5 us (20.5), fp32 53.4 (40.9), bf16 4096 x 1152 with an int8 checkpoint 10.3 (3.6), fp16
+// 8192 x 1280 17 (6.4); gradient bf16 8192 x 4096 38.6 (30.7), 4608 x 12288 70.7 (51.8), 4500 x 4096 from an int8
+// checkpoint 27.3 (14.2), 8192 x 640 13.5 (4.8).  The 16-bit forward and decoding issue for half of their time, and
+// the rest is a row's chain of two reductions with 32 warps per SM to cover it.  The fp16 forward spills at three
+// to five chunks a thread (up to 108 bytes a thread at K = 1032 to 1280), the gradient at four (36 to 104 bytes).
 #include <algorithm>
 #include <initializer_list>
 #include <type_traits>

@@ -13,13 +13,15 @@
 // is scaled by a power of two per token (largest magnitude to [2^13, 2^14)) and split into two fp16
 // columns, hi + lo: 22 significant bits, down to 2^-38 of the token's largest, so the inputs are
 // not rounded further than fp32 sums are.  The first kernel lays these columns out in the order the
-// second one's MMA fragments read them and computes T (bf16 inputs, exact products, fp32 sums).
+// second one's MMA fragments read them and computes T (bf16 inputs, exact products, fp32 sums), which enters
+// its product with L2 as three bf16 parts, all of its 24 bits.
 //
-// Measured (one B200, device time in a graph): NVFP4 1 x 4096 -> 24576, rank 32: 17.6 us, 3.3 TB/s, half
+// Measured (one B200, device time in a graph): NVFP4 1 x 4096 -> 24576, rank 32: 17.3-17.8 us, 3.3 TB/s, half
 // the copy rate.  Reading alone takes 14.3 us of it, the products alone 13.7, and 4.8 are in both (two
 // launches, the first kernel, the join): registers for three CTAs per SM leave the two to overlap only in
-// part.  Smaller layers are that fixed part: INT4 5 x 1280 -> 10240 10.8 us, NVFP4 16 x 10240 -> 1280 12.4,
-// 1 x 640 -> 640 5.4.
+// part, and 384 CTAs are three on 88 SMs and two on 60.  Smaller layers are that fixed part: INT4 5 x 1280 ->
+// 10240 10.6 us, NVFP4 16 x 10240 -> 1280 11.9, 1 x 640 -> 640 5.5.  For more than 4 tokens
+// 60 to 164 bytes a thread spill.
 //
 // Order of k.  A contraction may run in any order, so a thread takes 16 consecutive bytes (32
 // weights) of a row and feeds them to 8 MMA steps; the columns of X are laid out to match.
@@ -583,7 +585,8 @@ svdq_status launch_main(W4A16Params& p, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(kWarps) * kStages * kStageBytes +
                       static_cast<size_t>(kGroups) * NT * 4 * (kSlices * kUnitRows + 8) * sizeof(float) +
                       static_cast<size_t>(p.M) * p.r_pad * 3 * sizeof(uint16_t);
-  // as many CTAs as the SMs hold at a time, so that the units are dealt out evenly
+  // no more CTAs than the SMs hold at a time (dealt out evenly only where there are more pairs of units than that,
+  // or no more than SMs)
   const int resident = kSMs * (NT > 2 ? 2 : 3);
   const int grid = p.cluster > 1 || p.blocks < resident ? p.blocks : resident;
   static std::atomic<uint64_t> allowed{0};

@@ -12,9 +12,10 @@
 // not, and a code of 0 times an infinity is NaN.  (On the fragments: int8 4608 x 12288 20.4, 29.7 and 55.6 us at
 // r = 8, 32 and 64 against 20.2, 28.3 and 53.8 on the codes, E4M3 at r = 16 22.0 against 23.5.)
 //
-// Measured (one B200, device time in a graph): int8 4608 x 12288, r = 32: 29.7 us against 9.2 for one pass
-// over the bytes.  About 8 us are fixed (first copies, joins, second kernel), 13 the decoding and products
-// alone; the scale bytes, a sector each per row and 64 columns, cost 5.  bf16 4099 x 1152, r = 16: 6.9 us.
+// Measured (one B200, device time in a graph): int8 4608 x 12288, r = 32: 28.0 us against 9.2 for one pass
+// over the bytes, bf16 27.4 against 17.6.  About 8 us are fixed (first copies, joins, second kernel), 13 the
+// decoding and products alone; the scale bytes, a sector each per row and 64 columns, cost 5.  bf16 4099 x 1152,
+// r = 16: 7.0 us.  r = 64 and 128 take two and four passes (54 and 106 us from int8).
 //
 // A CTA holds its rows of S in shared memory; each warp copies its 16 x 64 tiles of X ahead through a
 // ring of its own, so the main loop has no CTA barrier.  Sums are joined by ordinary fp32 additions in
@@ -374,7 +375,7 @@ struct Plan {
 Plan plan(int M, int K, int r, int tile_rows) {
   Plan q{};
   const int tiles = (r + 7) / 8;
-  q.nt = tiles <= 1 ? 1 : tiles <= 2 ? 2 : 4;  // 8 would spill: at r = 64 102 us against 56 for two passes (4608 x 12288, int8)
+  q.nt = tiles <= 1 ? 1 : tiles <= 2 ? 2 : 4;  // 8 would spill: at r = 64 102 us against 54 for two passes (4608 x 12288, int8)
   q.zs = (tiles + q.nt - 1) / q.nt;
   q.col_warps = K >= 17 * 256 + 1 ? 4 : K >= 17 * 128 + 1 ? 2 : 1;
   q.blocks = (K + q.col_warps * kTileCols - 1) / (q.col_warps * kTileCols);
